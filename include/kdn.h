@@ -237,6 +237,96 @@ kdn_status_t kdn_backward(const kdn_problem_t *p,
                           float *dS0, float *dP0,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the plain sibling of the recurrence above
+ * (explainer, section "线性注意力": the additive write S + k v^T; with one decay per head instead of
+ * the delta rule's correction).  Per head, with a log decay g_t (natural logarithm, g_t <= 0;
+ * -infinity resets the memory),
+ *
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t        (readout after the write)
+ *
+ * Layouts, types, sizes, packed sequences, streams, errors and ownership are those of the head of
+ * this file; the log decay is always fp32.  Tokens behind the last packed sequence are neither read
+ * nor written.  A sequence never sees another one's rows, whatever they hold; within a sequence a
+ * non-finite input may also reach the outputs of the tokens shortly before it (those of its chunk,
+ * up to 127 tokens). */
+typedef enum {
+    KDN_DECAY_NONE = 0,    /* g = 0: plain linear attention (g is ignored) */
+    KDN_DECAY_TOKEN = 1,   /* g [B, T, H], one per token and head */
+    KDN_DECAY_HEAD = 2     /* g [H], one per head for all tokens */
+} kdn_decay_t;
+
+typedef struct {
+    int B, T, H, d_k, d_v;          /* varlen: B == 1 and T = total tokens */
+    const int32_t *cu_seqlens;      /* as in kdn_problem_t */
+    int num_seqs;
+    kdn_dtype_t in_dtype;           /* dtype of q, k, v and o (backward: of d_o, dq, dk and dv too) */
+    float scale;                    /* factor of the readout, finite */
+    int decay;                      /* kdn_decay_t */
+} kdn_linear_problem_t;
+
+/* Bytes of device workspace of kdn_linear_forward() (host-only). */
+kdn_status_t kdn_linear_workspace_size(const kdn_linear_problem_t *p, size_t *bytes);
+
+/* Forward over whole sequences (prompts, training), chunkwise.
+ *  q, k      : device [B, T, H, d_k];  v, o : device [B, T, H, d_v]     (in_dtype)
+ *  g         : device fp32, shape by `decay`
+ *  S0        : device fp32 [N, H, d_k, d_v] or NULL (zero);  S_out : the same, final states, or NULL;
+ *              they may not alias
+ *  workspace : device, >= kdn_linear_workspace_size() bytes, 256-byte aligned (contents on entry do
+ *              not matter; distinct per concurrent call).  Every other pointer 16-byte aligned. */
+kdn_status_t kdn_linear_forward(const kdn_linear_problem_t *p, const void *q, const void *k, const void *v,
+                                const float *g, const float *S0, void *o, float *S_out,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Recurrent form: n_tokens tokens of N independent sequences applied in order to the state, which is
+ * read once and written back once in place.
+ *  q, k : device [N, n_tokens, H, d_k];  v, o : device [N, n_tokens, H, d_v]   (in_dtype)
+ *  g    : device fp32 [N, n_tokens, H] or [H], by `decay` (kdn_decay_t)
+ *  S    : device fp32 [N, H, d_k, d_v], updated in place */
+kdn_status_t kdn_linear_decode_tokens(int N, int n_tokens, int H, int d_k, int d_v, kdn_dtype_t in_dtype, float scale,
+                                      int decay, const void *q, const void *k, const void *v, const float *g,
+                                      float *S, void *o, void *stream);
+
+/* Backward pass: gradients of  L = <o, d_o> + <S_T, dS_T>  with respect to every input, o and S_T as
+ * kdn_linear_forward() returns them for the same problem and inputs (which are all it needs: the
+ * states are formed again).
+ *  d_o        : device [B, T, H, d_v] (in_dtype);  dS_T : device fp32 [N, H, d_k, d_v] or NULL (zero)
+ *  dq, dk, dv : device, shapes of q, k, v, in_dtype: sums are fp32 and rounded once, to the type
+ *               that the projections' gradients read
+ *  dg         : device fp32, shape of g, or NULL (not written; must be NULL without a decay).  No
+ *               gradient is divided by a decay, so g = -infinity is fine (its gradient is 0).
+ *  dS0        : device fp32 [N, H, d_k, d_v] or NULL (not written); may not alias dS_T
+ *  workspace  : as for the forward, of kdn_linear_backward_workspace_size() bytes.
+ * Deterministic: no sum depends on the order in which blocks run. */
+kdn_status_t kdn_linear_backward_workspace_size(const kdn_linear_problem_t *p, size_t *bytes);
+kdn_status_t kdn_linear_backward(const kdn_linear_problem_t *p, const void *q, const void *k, const void *v,
+                                 const float *g, const float *S0, const void *d_o, const float *dS_T,
+                                 void *dq, void *dk, void *dv, float *dg, float *dS0,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* Layer norm over the last axis of n x G rows of d elements ([n, G, d], contiguous), with a weight
+ * and a bias row for each of the G groups: G = 1 for one pair of rows [d], G = H for the norm of a
+ * layer's readout o [B, T, H, d_v] (n = B T), whose size, unlike that of the delta rule's, the
+ * recurrence does not bound.
+ *     m = mean(x),  r = (mean((x - m)^2) + eps)^(-1/2),  y = (x - m) r * weight + bias
+ *  x, y         : device [n, G, d] (dtype);  weight, bias : device fp32 [G, d], or NULL (1, 0)
+ *  mean, rstd   : device fp32 [n, G], m and r for the backward, or NULL (not written)
+ * 1 <= d <= 16384, G <= 65535, eps >= 0; every pointer 16-byte aligned. */
+kdn_status_t kdn_layer_norm(long long n, int G, int d, kdn_dtype_t dtype, float eps, const void *x,
+                            const float *weight, const float *bias, void *y, float *mean, float *rstd, void *stream);
+
+/* Backward of kdn_layer_norm(): gradients of <y, dy>.
+ *  dy, x, dx      : device [n, G, d] (dtype);  mean, rstd : device fp32 [n, G], as the forward left them
+ *  dweight, dbias : device fp32 [G, d], sums over the n rows, or NULL (not written)
+ *  workspace      : device, >= kdn_layer_norm_backward_workspace_size() bytes, 256-byte aligned; NULL
+ *                   is fine without dweight and dbias.
+ * Deterministic: the sums over rows do not depend on the order in which blocks run. */
+kdn_status_t kdn_layer_norm_backward_workspace_size(long long n, int G, int d, size_t *bytes);
+kdn_status_t kdn_layer_norm_backward(long long n, int G, int d, kdn_dtype_t dtype, const void *dy, const void *x,
+                                     const float *weight, const float *mean, const float *rstd, void *dx,
+                                     float *dweight, float *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Which execution path kdn_forward_chunkwise() takes for `p` (host-only; no CUDA call
  * besides resolving the driver's tensor-map encoder once): 0 token-serial recurrence,
  * 1 fp32 CUDA-core chunk kernel, 3 the tcgen05 tensor-core path in two launches (taken when

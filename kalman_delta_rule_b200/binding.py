@@ -35,10 +35,20 @@ class kdn_problem_t(ctypes.Structure):
                 ("max_seqlen", ctypes.c_int), ("variant", ctypes.c_int)]
 
 
+class kdn_linear_problem_t(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("d_k", ctypes.c_int),
+                ("d_v", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("scale", ctypes.c_float), ("decay", ctypes.c_int)]
+
+
+KDN_DECAY_NONE, KDN_DECAY_TOKEN, KDN_DECAY_HEAD = 0, 1, 2
+
 _lib = None
 _lock = threading.Lock()
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _PP = ctypes.POINTER(kdn_problem_t)
+_PL = ctypes.POINTER(kdn_linear_problem_t)
+_ll, _psz = ctypes.c_longlong, ctypes.POINTER(_sz)
 
 _SIGS = {
     "kdn_workspace_size": (_i, [_PP, ctypes.POINTER(_sz)]),
@@ -54,6 +64,14 @@ _SIGS = {
     "kdn_execution_path": (_i, [_PP]),
     "kdn_gain_scan_noalloc": (_i, [_PP] + [_vp] * 4 + [_vp] + [_vp] * 3 + [_vp]),
     "kdn_backward_workspace_size": (_i, [_PP, ctypes.POINTER(_sz)]),
+    "kdn_linear_workspace_size": (_i, [_PL, _psz]),
+    "kdn_linear_forward": (_i, [_PL] + [_vp] * 7 + [_vp, _sz, _vp]),
+    "kdn_linear_decode_tokens": (_i, [_i] * 6 + [_f, _i] + [_vp] * 6 + [_vp]),
+    "kdn_linear_backward_workspace_size": (_i, [_PL, _psz]),
+    "kdn_linear_backward": (_i, [_PL] + [_vp] * 12 + [_vp, _sz, _vp]),
+    "kdn_layer_norm": (_i, [_ll, _i, _i, _i, _f] + [_vp] * 6 + [_vp]),
+    "kdn_layer_norm_backward_workspace_size": (_i, [_ll, _i, _i, _psz]),
+    "kdn_layer_norm_backward": (_i, [_ll, _i, _i, _i] + [_vp] * 8 + [_vp, _sz, _vp]),
     "kdn_backward": (_i, [_PP] + [_vp] * 6 + [_vp] * 2 + [_vp] * 3 + [_vp] * 6 + [_vp] * 2 + [_vp, _sz, _vp]),
 }
 
@@ -124,6 +142,48 @@ def kdn_backward(problem, q, k, v, alpha, sigma, r, S0, P0, d_o, dS_T, dP_T, dq,
                  dS0, dP0, workspace, workspace_bytes, stream):
     return load().kdn_backward(ctypes.byref(problem), q, k, v, alpha, sigma, r, S0, P0, d_o, dS_T, dP_T,
                                dq, dk, dv, dalpha, dsigma, dr, dS0, dP0, workspace, workspace_bytes, stream)
+
+
+def kdn_linear_workspace_size(problem: kdn_linear_problem_t) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().kdn_linear_workspace_size(ctypes.byref(problem), ctypes.byref(n)), "kdn_linear_workspace_size")
+    return n.value
+
+
+def kdn_linear_forward(problem, q, k, v, g, S0, o, S_out, workspace, workspace_bytes, stream):
+    return load().kdn_linear_forward(ctypes.byref(problem), q, k, v, g, S0, o, S_out, workspace, workspace_bytes, stream)
+
+
+def kdn_linear_decode_tokens(N, n_tokens, H, d_k, d_v, in_dtype, scale, decay, q, k, v, g, S, o, stream):
+    return load().kdn_linear_decode_tokens(N, n_tokens, H, d_k, d_v, in_dtype, scale, decay, q, k, v, g, S, o, stream)
+
+
+def kdn_linear_backward_workspace_size(problem: kdn_linear_problem_t) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().kdn_linear_backward_workspace_size(ctypes.byref(problem), ctypes.byref(n)),
+           "kdn_linear_backward_workspace_size")
+    return n.value
+
+
+def kdn_linear_backward(problem, q, k, v, g, S0, d_o, dS_T, dq, dk, dv, dg, dS0, workspace, workspace_bytes, stream):
+    return load().kdn_linear_backward(ctypes.byref(problem), q, k, v, g, S0, d_o, dS_T, dq, dk, dv, dg, dS0,
+                                      workspace, workspace_bytes, stream)
+
+
+def kdn_layer_norm(n, G, d, dtype, eps, x, weight, bias, y, mean, rstd, stream):
+    return load().kdn_layer_norm(n, G, d, dtype, eps, x, weight, bias, y, mean, rstd, stream)
+
+
+def kdn_layer_norm_backward_workspace_size(n: int, G: int, d: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(load().kdn_layer_norm_backward_workspace_size(n, G, d, ctypes.byref(b)), "kdn_layer_norm_backward_workspace_size")
+    return b.value
+
+
+def kdn_layer_norm_backward(n, G, d, dtype, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, workspace_bytes,
+                            stream):
+    return load().kdn_layer_norm_backward(n, G, d, dtype, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace,
+                                          workspace_bytes, stream)
 
 
 def kdn_last_device_error(stream=None) -> int:
@@ -309,6 +369,243 @@ def gain_scan(k, alpha, sigma, r, cu_seqlens=None, P0=None, mu: float = 1.0, chu
                        _ptr(workspace), wbytes, _stream_handle(stream))
     _check(st, "kdn_gain_scan")
     return g, be, P_out
+
+
+# ------------------------------------------------------------------ linear attention, layer norm
+_DTYPES = {"torch.bfloat16": KDN_DTYPE_BF16, "torch.float32": KDN_DTYPE_F32}
+
+
+def _expect(name, t, shape, dtype, device):
+    """Raise unless ``t`` is a contiguous tensor of this shape, type and device."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected {device} (CUDA)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _type_of(name, t):
+    code = _DTYPES.get(str(t.dtype))
+    if code is None:
+        raise TypeError(f"{name} is {t.dtype} (float32 or bfloat16 expected)")
+    return code
+
+
+def _dptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _On:
+    """The tensors' device and the caller's stream made current: outputs and workspace come from that
+    stream's allocator, and the kernels are launched on it.  ``stream`` None is that device's current one."""
+
+    def __init__(self, torch, device, stream):
+        self.torch, self.device, self.stream = torch, device, stream
+
+    def __enter__(self):
+        torch = self.torch
+        self.ctx = None
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
+            self.ctx = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != self.device.index:
+            self.ctx = torch.cuda.device(self.device)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream()
+        return s.cuda_stream or None
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _linear_problem(q, k, v, g, cu_seqlens, scale):
+    torch = _torch()
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be [B, T, H, d]")
+    B, T, H, dk = q.shape
+    dev = q.device
+    p = kdn_linear_problem_t()
+    p.in_dtype = _type_of("q", q)
+    _expect("q", q, q.shape, q.dtype, dev)
+    _expect("k", k, q.shape, q.dtype, dev)
+    _expect("v", v, (B, T, H, v.shape[-1]), q.dtype, dev)
+    p.B, p.T, p.H, p.d_k, p.d_v, p.scale = B, T, H, dk, v.shape[-1], float(scale)
+    p.num_seqs = B
+    if cu_seqlens is not None:
+        _expect("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32, dev)
+        if cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens needs at least one entry")
+        if B != 1:
+            raise ValueError("packed sequences need B = 1")
+        p.num_seqs = cu_seqlens.numel() - 1
+        # without sequences the pointer would be all that marks the problem as packed
+        p.cu_seqlens = cu_seqlens.data_ptr()
+    if g is not None:
+        p.decay = KDN_DECAY_HEAD if g.dim() == 1 else KDN_DECAY_TOKEN
+        _expect("g", g, (H,) if g.dim() == 1 else (B, T, H), torch.float32, dev)
+    return torch, p
+
+
+def _linear_state(torch, name, t, p, dev):
+    if t is not None:
+        _expect(name, t, (p.num_seqs, p.H, p.d_k, p.d_v), torch.float32, dev)
+
+
+def _bytes(torch, n, dev):
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def linear_forward(q, k, v, g=None, cu_seqlens=None, S0=None, scale: float = 1.0, o=None, S_out=None,
+                   want_state: bool = True, workspace=None, stream=None):
+    """Linear attention with a decay for each head over whole sequences (kdn_linear_forward):
+    S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q, k [B,T,H,dk] and v [B,T,H,dv] in bf16 or fp32; g the fp32 log decay, [B,T,H], [H] or None (no
+    decay); varlen: B = 1 with int32 cu_seqlens; S0 [N,H,dk,dv] fp32.  Returns (o, S_out); outputs
+    and workspace are allocated when not given (S_out stays None without ``want_state``)."""
+    torch, p = _linear_problem(q, k, v, g, cu_seqlens, scale)
+    dev = q.device
+    _linear_state(torch, "S0", S0, p, dev)
+    with _On(torch, dev, stream) as handle:
+        if o is None:
+            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
+        else:
+            _expect("o", o, v.shape, q.dtype, dev)
+        if S_out is None and want_state:
+            S_out = torch.empty((p.num_seqs, p.H, p.d_k, p.d_v), dtype=torch.float32, device=dev)
+        else:
+            _linear_state(torch, "S_out", S_out, p, dev)
+        if workspace is None:
+            workspace = _bytes(torch, kdn_linear_workspace_size(p), dev)
+        st = kdn_linear_forward(p, _dptr(q), _dptr(k), _dptr(v), _dptr(g), _dptr(S0), _dptr(o), _dptr(S_out),
+                                _ptr(workspace), workspace.numel() * workspace.element_size(), handle)
+    _check(st, "kdn_linear_forward")
+    return o, S_out
+
+
+def linear_decode_tokens(q, k, v, g, S, scale: float = 1.0, o=None, stream=None):
+    """n tokens per sequence of the recurrent form in one launch on [N, n, H, d] token tensors
+    (kdn_linear_decode_tokens); g [N, n, H], [H] or None; S [N,H,dk,dv] fp32, updated in place."""
+    torch, p = _linear_problem(q, k, v, g, None, scale)
+    dev = q.device
+    _linear_state(torch, "S", S, p, dev)
+    with _On(torch, dev, stream) as handle:
+        if o is None:
+            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
+        else:
+            _expect("o", o, v.shape, q.dtype, dev)
+        st = kdn_linear_decode_tokens(p.B, p.T, p.H, p.d_k, p.d_v, p.in_dtype, p.scale, p.decay, _dptr(q), _dptr(k),
+                                      _dptr(v), _dptr(g), _dptr(S), _dptr(o), handle)
+    _check(st, "kdn_linear_decode_tokens")
+    return o
+
+
+def linear_decode_step(q, k, v, g, S, scale: float = 1.0, o=None, stream=None):
+    """One token of the recurrent form on [N, H, d] token tensors; g [N, H], [H] or None.  A one-dimensional
+    g is the per-head decay."""
+    g4 = g if g is None or g.dim() == 1 else g.unsqueeze(1)
+    o4 = None if o is None else o.unsqueeze(1)
+    return linear_decode_tokens(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g4, S, scale=scale, o=o4,
+                                stream=stream).squeeze(1)
+
+
+def linear_backward(q, k, v, g, d_o, cu_seqlens=None, S0=None, dS=None, scale: float = 1.0, want_initial: bool = True,
+                    workspace=None, stream=None):
+    """Gradients of <o, d_o> + <S_T, dS> for ``linear_forward``'s inputs (kdn_linear_backward).
+
+    Returns a dict: dq, dk, dv (shapes and type of q, k, v), with a decay dg (fp32, shape of g), and with
+    ``want_initial`` dS0 [N,H,dk,dv] fp32.  The workspace is allocated when not given."""
+    torch, p = _linear_problem(q, k, v, g, cu_seqlens, scale)
+    dev = q.device
+    _expect("d_o", d_o, v.shape, q.dtype, dev)
+    _linear_state(torch, "S0", S0, p, dev)
+    _linear_state(torch, "dS", dS, p, dev)
+    with _On(torch, dev, stream) as handle:
+        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
+        if g is not None:
+            out["dg"] = torch.empty_like(g)
+        if want_initial:
+            out["dS0"] = torch.empty((p.num_seqs, p.H, p.d_k, p.d_v), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = _bytes(torch, kdn_linear_backward_workspace_size(p), dev)
+        st = kdn_linear_backward(p, _dptr(q), _dptr(k), _dptr(v), _dptr(g), _dptr(S0), _dptr(d_o), _dptr(dS),
+                                 _dptr(out["dq"]), _dptr(out["dk"]), _dptr(out["dv"]), _dptr(out.get("dg")),
+                                 _dptr(out.get("dS0")), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                 handle)
+    _check(st, "kdn_linear_backward")
+    return out
+
+
+def _norm_rows(x, weight):
+    """(rows n, groups G, width d): with a [G, d] weight the rows are [..., G, d], else one group."""
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    d = x.shape[-1]
+    G = 1
+    if weight is not None and weight.dim() == 2:
+        G = weight.shape[0]
+        if x.dim() < 2 or x.shape[-2] != G:
+            raise ValueError(f"a weight of {G} groups needs x [..., {G}, {d}], got {tuple(x.shape)}")
+    return (x.numel() // (G * d) if G * d else 0), G, d
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, y=None, stream=None):
+    """Layer norm over the last axis (kdn_layer_norm); returns (y, mean, rstd), mean and rstd fp32 of
+    x.shape[:-1].  weight, bias: fp32 [d], or [G, d] for x [..., G, d] (a row for each head), or None."""
+    torch = _torch()
+    code = _type_of("x", x)
+    dev = x.device
+    _expect("x", x, x.shape, x.dtype, dev)
+    n, G, d = _norm_rows(x, weight if weight is not None else bias)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _expect(name, t, (G, d) if t.dim() == 2 else (d,), torch.float32, dev)
+            if t.numel() != G * d:
+                raise ValueError("weight and bias must have the same shape")
+    with _On(torch, dev, stream) as handle:
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _expect("y", y, x.shape, x.dtype, dev)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty_like(mean)
+        st = kdn_layer_norm(n, G, d, code, float(eps), _dptr(x), _dptr(weight), _dptr(bias), _dptr(y), _dptr(mean),
+                            _dptr(rstd), handle)
+    _check(st, "kdn_layer_norm")
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, workspace=None, stream=None):
+    """Gradients of <y, dy> for ``layer_norm`` (kdn_layer_norm_backward), mean and rstd as it returned
+    them: a dict of dx and, with a weight, dweight and dbias (fp32, the weight's shape)."""
+    torch = _torch()
+    code = _type_of("x", x)
+    dev = x.device
+    _expect("x", x, x.shape, x.dtype, dev)
+    _expect("dy", dy, x.shape, x.dtype, dev)
+    n, G, d = _norm_rows(x, weight)
+    if weight is not None:
+        _expect("weight", weight, (G, d) if weight.dim() == 2 else (d,), torch.float32, dev)
+    _expect("mean", mean, x.shape[:-1], torch.float32, dev)
+    _expect("rstd", rstd, x.shape[:-1], torch.float32, dev)
+    with _On(torch, dev, stream) as handle:
+        out = {"dx": torch.empty_like(x)}
+        if weight is not None:
+            out["dweight"], out["dbias"] = torch.empty_like(weight), torch.empty_like(weight)
+            if workspace is None:
+                workspace = _bytes(torch, kdn_layer_norm_backward_workspace_size(n, G, d), dev)
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = kdn_layer_norm_backward(n, G, d, code, _dptr(dy), _dptr(x), _dptr(weight), _dptr(mean), _dptr(rstd),
+                                     _dptr(out["dx"]), _dptr(out.get("dweight")), _dptr(out.get("dbias")),
+                                     _ptr(workspace), wbytes, handle)
+    _check(st, "kdn_layer_norm_backward")
+    return out
 
 
 PATH_NAMES = {0: "recurrent", 1: "chunk_fp32", 3: "chunk_tcgen05_two_phase"}

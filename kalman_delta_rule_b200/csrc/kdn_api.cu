@@ -69,6 +69,10 @@ size_t two_phase_bytes(const kdn_problem_t *p, const Resolved &rv) {
 
 }  // namespace
 
+namespace kdn {
+unsigned *error_word() { return err_word(); }
+}  // namespace kdn
+
 extern "C" {
 
 const char *kdn_status_string(kdn_status_t s) {

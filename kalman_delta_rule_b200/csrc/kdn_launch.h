@@ -6,6 +6,7 @@
 #include <stddef.h>
 
 #include "kdn_common.cuh"
+#include "kdn_linear.cuh"
 
 namespace kdn {
 
@@ -20,6 +21,9 @@ cudaError_t kernel_setup(const void *kern, size_t smem, int threads, bool max_ca
 // Device address of a __device__ symbol on the current device and context, looked up once
 // (with that device current) and cached; looked up again after the context changes.
 cudaError_t symbol_address(const void *symbol, void **out);
+
+// The current device's error word (bits ERR_*), or NULL if its address cannot be had.
+unsigned *error_word();
 
 // token-serial fused recurrence; dvt = d_v tile per CTA (32/64/128/256, divides d_v)
 cudaError_t launch_recurrent(const TokenArgs &a, bool bf16_in, int dvt, cudaStream_t st);
@@ -65,5 +69,31 @@ cudaError_t launch_gain_scan_noalloc(const ScanArgs &a, bool bf16_in, long long 
 bool gain_scan_tma_supported(int dk, bool bf16_in);
 size_t scan_tma_workspace_bytes(long long nchains, long long nchunks_max);
 cudaError_t launch_gain_scan_tma(const ScanArgs &a, long long ntok, void *workspace, cudaStream_t st);
+
+// ---- linear attention with a decay for each head
+// fp32 CUDA-core path in chunks of 64 tokens: chunk contributions, their scan, outputs / gradients
+size_t linear_simt_workspace_bytes(const LinArgs &a);
+size_t linear_simt_backward_workspace_bytes(const LinArgs &a);
+cudaError_t launch_linear_simt(const LinArgs &a, bool bf16_in, void *workspace, cudaStream_t st);
+cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, bool bf16_in, void *workspace, cudaStream_t st);
+// n tokens of N sequences on a state updated in place
+cudaError_t launch_linear_decode(const LinArgs &a, bool bf16_in, cudaStream_t st);
+
+// ---- layer norm of rows [n, G, d] with a weight and bias row for each of G groups
+struct NormArgs {
+    const void *x, *dy;                  // [n, G, d]
+    const float *weight, *bias;          // [G, d] or NULL (1, 0)
+    void *y, *dx;                        // [n, G, d]
+    float *mean, *rstd;                  // [n, G]; written by the forward (may be NULL), read by the backward
+    float *dweight, *dbias;              // [G, d]; either may be NULL
+    float *part;                         // workspace: the blocks' shares of dweight and dbias
+    long long n;
+    int G, d;
+    float eps;
+};
+constexpr int kNormMaxWidth = 16384;
+size_t norm_backward_workspace_bytes(long long n, int G, int d);
+cudaError_t launch_norm(const NormArgs &a, bool bf16_in, cudaStream_t st);
+cudaError_t launch_norm_backward(const NormArgs &a, bool bf16_in, cudaStream_t st);
 
 }  // namespace kdn

@@ -1,0 +1,512 @@
+// Linear attention with a decay for each head on CUDA cores, fp32 arithmetic, in chunks of 64 tokens
+// (the recurrence unrolled as in kdn_linear.cuh).  Every step is parallel over chunks but one:
+//   delta  per (chunk, head, d_v tile): the chunk's own contribution U = K^T diag(w) V (w = decay to
+//          the chunk's end) or, for the gradient, E = scale Q^T diag(e^G) dO, and the chunk's decay
+//   scan   per state element: the contributions become the states at the chunks' starts
+//          (S <- decay S + U, forwards), or the state gradients at the chunks' ends (backwards)
+//   out    per (chunk, head, d_v tile): o
+//   grad   per (chunk, head): dq, dk, dv and the decay's gradient
+// The scan reads and writes each chunk's state once, which costs about the token tensors' own
+// traffic at d = 128, and in exchange no step but its multiply-add chain is serial: a problem of
+// few, long sequences fills the GPU as well as one of many short ones.
+#include "kdn_common.cuh"
+#include "kdn_launch.h"
+
+namespace kdn {
+
+namespace {
+
+constexpr int C = 64;          // tokens of a chunk
+constexpr int NT = 256;
+constexpr int PAD = 4;         // floats behind each shared-memory row: 16 rows' float4 reads hit 16 banks groups
+
+__device__ __forceinline__ float4 scale4(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
+
+// acc[i][j] += sum_k A(m_i, k) B(k, n_j) for m_i = 4 ty + i, n_j = tx + 16 j (16 x 16 threads).
+// TA: A is stored [k][m]; TB: B is stored [n][k].  Row strides lda, ldb; K a multiple of 4.
+template <int NJ, bool TA, bool TB>
+__device__ __forceinline__ void mm(float (&acc)[4][NJ], const float *A, int lda, const float *B, int ldb, int K, int ty,
+                                   int tx) {
+#pragma unroll 2
+    for (int k = 0; k < K; k += 4) {
+        float av[4][4];        // [i][k]
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = TA ? *reinterpret_cast<const float4 *>(A + (k + i) * lda + ty * 4)
+                                : *reinterpret_cast<const float4 *>(A + (ty * 4 + i) * lda + k);
+            const float e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                if (TA) av[m][i] = e[m]; else av[i][m] = e[m];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            float bv[4];
+            if (TB) {
+                const float4 x = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + k);
+                bv[0] = x.x; bv[1] = x.y; bv[2] = x.z; bv[3] = x.w;
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) bv[kk] = B[(k + kk) * ldb + tx + 16 * j];
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][j] = fmaf(av[i][kk], bv[kk], acc[i][j]);
+        }
+    }
+}
+
+// rows [0, L) of W columns from a token tensor ([ntok, H, d], column col) to shared memory [C][W + PAD];
+// rows behind the piece's end are zero, whatever the next sequence's rows hold
+template <int W, typename Tin>
+__device__ __forceinline__ void load_rows(float *dst, const void *src, int tok, int L, int H, int h, int d, int col) {
+    const Tin *p = static_cast<const Tin *>(src) + ((size_t)tok * H + h) * d + col;
+    const size_t rs = (size_t)H * d;
+    for (int i = threadIdx.x; i < C * (W / 4); i += NT) {
+        const int r = i / (W / 4), c = (i % (W / 4)) * 4;
+        *reinterpret_cast<float4 *>(dst + r * (W + PAD) + c) = r < L ? ldf4(p + r * rs + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+// a [DK][W] block of a state (row stride dv) to shared memory [DK][W + PAD]
+template <int DK, int W>
+__device__ __forceinline__ void load_state(float *dst, const float *src, int dv) {
+    for (int i = threadIdx.x; i < DK * (W / 4); i += NT) {
+        const int r = i / (W / 4), c = (i % (W / 4)) * 4;
+        *reinterpret_cast<float4 *>(dst + r * (W + PAD) + c) = *reinterpret_cast<const float4 *>(src + (size_t)r * dv + c);
+    }
+}
+
+// G (log2, inclusive) of the chunk's C tokens to shared memory by warp 0; decay 1 behind the end
+__device__ __forceinline__ void chunk_log_decay(const LinArgs &a, int tok, int L, int h, double *G) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        double x0 = 2 * lane < L ? lin_log2_decay(a, tok + 2 * lane, h) : 0.0;
+        double x1 = x0 + (2 * lane + 1 < L ? lin_log2_decay(a, tok + 2 * lane + 1, h) : 0.0);
+        double s = x1;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, s, off);
+            if (lane >= off) s += y;
+        }
+        const double before = s - x1;
+        G[2 * lane] = before + x0;
+        G[2 * lane + 1] = s;
+    }
+    __syncthreads();
+}
+
+// sum over the 16 threads of a row (lanes tx = 0..15)
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+struct Ws {
+    float *U, *E;              // [slots, H, dk, dv]: states at the chunks' starts; state gradients at their ends
+    float2 *dec;               // [slots, H] decay of the whole chunk
+    float *dgc;                // [slots, H] the chunk's share of a per-head decay's gradient
+};
+
+}  // namespace
+
+// ------------------------------------------------------------------ delta
+template <int DK, int DVT, typename Tin, bool REV>
+__global__ void __launch_bounds__(NT) linear_delta_kernel(LinArgs a, const void *X, const void *Y, float *out, float2 *dec)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *Xs = sm, *Ys = sm + C * (DK + PAD);
+    __shared__ double G[C];
+    const int u = blockIdx.x / a.H, h = blockIdx.x % a.H, col = blockIdx.y * DVT;
+    LinPiece p;
+    if (!lin_piece(a, u, C, p) || p.len == 0) return;
+    const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
+    load_rows<DK, Tin>(Xs, X, tok, L, a.H, h, DK, 0);
+    load_rows<DVT, Tin>(Ys, Y, tok, L, a.H, h, a.dv, col);
+    chunk_log_decay(a, tok, L, h, G);
+    for (int i = threadIdx.x; i < L * (DVT / 4); i += NT) {
+        const int r = i / (DVT / 4);
+        float4 *y = reinterpret_cast<float4 *>(Ys + r * (DVT + PAD) + (i % (DVT / 4)) * 4);
+        *y = scale4(*y, REV ? a.scale * lin_exp2(G[r]) : lin_exp2(G[C - 1] - G[r]));
+    }
+    if (blockIdx.y == 0 && threadIdx.x == 0) dec[(size_t)u * a.H + h] = lin_chunk_decay(G[C - 1]);
+    __syncthreads();
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    float *dst = out + ((size_t)u * a.H + h) * DK * a.dv + col;
+#pragma unroll
+    for (int m0 = 0; m0 < DK; m0 += 64) {
+        if (ty * 4 >= DK) break;
+        float acc[4][DVT / 16] = {};
+        mm<DVT / 16, true, false>(acc, Xs + m0, DK + PAD, Ys, DVT + PAD, C, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < DVT / 16; ++j) dst[(size_t)(m0 + ty * 4 + i) * a.dv + tx + 16 * j] = acc[i][j];
+    }
+}
+
+// ------------------------------------------------------------------ scan
+// thread = four elements of one (sequence, head)'s state; the chunks' contributions are fetched
+// eight at a time, so that the loads of a group overlap and only its multiply-adds are serial
+template <bool REV>
+__global__ void __launch_bounds__(256) linear_scan_kernel(LinArgs a, float *U, const float2 *dec, const float *first, float *last)
+{
+    const int per = a.dk * a.dv / 4;
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int sh = (int)(id / per), e = (int)(id % per) * 4;
+    if (sh >= a.nseq * a.H) return;
+    const int s = sh / a.H, h = sh % a.H;
+    int t0, len;
+    lin_seq(a, s, t0, len);
+    const int n = (len + C - 1) / C;
+    const size_t st = (size_t)a.H * a.dk * a.dv;
+    float *p = U + ((size_t)lin_first_slot(a, s, t0, C) * a.H + h) * a.dk * a.dv + e;
+    const float2 *d = dec + (size_t)lin_first_slot(a, s, t0, C) * a.H + h;
+    const size_t se = (size_t)sh * a.dk * a.dv + e;
+    float4 x = first ? *reinterpret_cast<const float4 *>(first + se) : make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int B = 8;
+    for (int c0 = 0; c0 < n; c0 += B) {
+        float4 y[B];
+        float2 f[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (c0 + i < n) {
+                const int c = REV ? n - 1 - c0 - i : c0 + i;
+                y[i] = *reinterpret_cast<const float4 *>(p + c * st);
+                f[i] = d[(size_t)c * a.H];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (c0 + i < n) {
+                const int c = REV ? n - 1 - c0 - i : c0 + i;
+                *reinterpret_cast<float4 *>(p + c * st) = x;
+                x = make_float4(lin_carry(f[i], x.x, y[i].x), lin_carry(f[i], x.y, y[i].y), lin_carry(f[i], x.z, y[i].z),
+                                lin_carry(f[i], x.w, y[i].w));
+            }
+        }
+    }
+    if (last) *reinterpret_cast<float4 *>(last + se) = x;
+}
+
+// ------------------------------------------------------------------ out
+template <int DK, int DVT, typename Tin>
+__global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *S)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *Qs = sm, *Ks = Qs + C * (DK + PAD), *Vs = Ks + C * (DK + PAD), *Ss = Vs + C * (DVT + PAD),
+          *Ps = Ss + DK * (DVT + PAD);
+    __shared__ double G[C];
+    const int u = blockIdx.x / a.H, h = blockIdx.x % a.H, col = blockIdx.y * DVT;
+    LinPiece p;
+    if (!lin_piece(a, u, C, p) || p.len == 0) return;
+    const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
+    load_rows<DK, Tin>(Qs, a.q, tok, L, a.H, h, DK, 0);
+    load_rows<DK, Tin>(Ks, a.k, tok, L, a.H, h, DK, 0);
+    load_rows<DVT, Tin>(Vs, a.v, tok, L, a.H, h, a.dv, col);
+    load_state<DK, DVT>(Ss, S + ((size_t)u * a.H + h) * DK * a.dv + col, a.dv);
+    chunk_log_decay(a, tok, L, h, G);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    {
+        float acc[4][4] = {};
+        mm<4, false, true>(acc, Qs, DK + PAD, Ks, DK + PAD, DK, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = ty * 4 + i, s = tx + 16 * j;
+                Ps[t * (C + PAD) + s] = s <= t ? a.scale * acc[i][j] * lin_exp2(G[t] - G[s]) : 0.f;
+            }
+    }
+    __syncthreads();
+    float acc[4][DVT / 16] = {};
+    mm<DVT / 16, false, false>(acc, Qs, DK + PAD, Ss, DVT + PAD, DK, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f = a.scale * lin_exp2(G[ty * 4 + i]);
+#pragma unroll
+        for (int j = 0; j < DVT / 16; ++j) acc[i][j] *= f;
+    }
+    mm<DVT / 16, false, false>(acc, Ps, C + PAD, Vs, DVT + PAD, C, ty, tx);
+    Tin *o = static_cast<Tin *>(a.o) + ((size_t)tok * a.H + h) * a.dv + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = ty * 4 + i;
+        if (t >= L) continue;
+#pragma unroll
+        for (int j = 0; j < DVT / 16; ++j) stf(o + (size_t)t * a.H * a.dv + tx + 16 * j, acc[i][j]);
+    }
+}
+
+// ------------------------------------------------------------------ grad
+// With P = scale QK^T o D, dP = dO V^T, dA = scale dP o D, Z = P o dP, S the state at the chunk's start,
+// R the gradient of the state at its end, a_t = scale e^{G_t}, w_t = e^{G_C - G_t}:
+//   dQ = dA K + a (dO S^T),  dK = dA^T Q + w (V R^T),  dV = P^T dO + w (K R)
+//   dg_t = sum over pairs (query i >= t, key j < t), in the chunk, before and behind it:
+//        sum_{s >= t} (rows Z - columns Z)_s + sum_{s >= t} q_s.(a dO S^T)_s + sum_{s < t} k_s.(w V R^T)_s + e^{G_C} <S, R>
+// No term is divided by a decay, and none of the four cancels against another.
+template <int DK, int DVT, typename Tin>
+__global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
+{
+    const LinArgs &a = b.a;
+    constexpr int NK = DK / 16, NV = DVT / 16;
+    extern __shared__ __align__(16) float sm[];
+    float *Qs = sm, *Ks = Qs + C * (DK + PAD), *Vs = Ks + C * (DK + PAD), *Os = Vs + C * (DVT + PAD),
+          *Ss = Os + C * (DVT + PAD), *Rs = Ss + DK * (DVT + PAD), *Ps = Rs + DK * (DVT + PAD), *As = Ps + C * (C + PAD);
+    __shared__ double G[C];
+    __shared__ float zr[C], zc[8][C], xi[C], yi[C], wsum[8];
+    const int u = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    LinPiece p;
+    if (!lin_piece(a, u, C, p) || p.len == 0) return;
+    const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const size_t sbase = ((size_t)u * a.H + h) * DK * a.dv;
+    load_rows<DK, Tin>(Qs, a.q, tok, L, a.H, h, DK, 0);
+    load_rows<DK, Tin>(Ks, a.k, tok, L, a.H, h, DK, 0);
+    chunk_log_decay(a, tok, L, h, G);
+
+    float pv[4][4] = {};
+    mm<4, false, true>(pv, Qs, DK + PAD, Ks, DK + PAD, DK, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = ty * 4 + i, s = tx + 16 * j;
+            pv[i][j] = s <= t ? a.scale * pv[i][j] * lin_exp2(G[t] - G[s]) : 0.f;
+            Ps[t * (C + PAD) + s] = pv[i][j];
+        }
+
+    float dp[4][4] = {}, dqi[4][NK] = {}, dki[4][NK] = {};
+    float sr = 0.f;
+    for (int col = 0; col < a.dv; col += DVT) {
+        __syncthreads();       // the previous tile is read; Ps is written
+        load_rows<DVT, Tin>(Vs, a.v, tok, L, a.H, h, a.dv, col);
+        load_rows<DVT, Tin>(Os, b.d_o, tok, L, a.H, h, a.dv, col);
+        load_state<DK, DVT>(Ss, ws.U + sbase + col, a.dv);
+        load_state<DK, DVT>(Rs, ws.E + sbase + col, a.dv);
+        __syncthreads();
+        for (int i = threadIdx.x; i < DK * DVT; i += NT) {
+            const int e = (i / DVT) * (DVT + PAD) + i % DVT;
+            sr = fmaf(Ss[e], Rs[e], sr);
+        }
+        mm<4, false, true>(dp, Os, DVT + PAD, Vs, DVT + PAD, DVT, ty, tx);
+        mm<NK, false, true>(dqi, Os, DVT + PAD, Ss, DVT + PAD, DVT, ty, tx);
+        mm<NK, false, true>(dki, Vs, DVT + PAD, Rs, DVT + PAD, DVT, ty, tx);
+        float acc[4][NV] = {};
+        mm<NV, false, false>(acc, Ks, DK + PAD, Rs, DVT + PAD, DK, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float w = lin_exp2(G[C - 1] - G[ty * 4 + i]);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) acc[i][j] *= w;
+        }
+        mm<NV, true, false>(acc, Ps, C + PAD, Os, DVT + PAD, C, ty, tx);
+        Tin *dv = static_cast<Tin *>(b.dv) + ((size_t)tok * a.H + h) * a.dv + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = ty * 4 + i;
+            if (t >= L) continue;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) stf(dv + (size_t)t * a.H * a.dv + tx + 16 * j, acc[i][j]);
+        }
+    }
+
+    // ---- dA to shared memory; rows and columns of Z; the boundary terms of the decay's gradient
+    float zcol[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = ty * 4 + i;
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int s = tx + 16 * j;
+            As[t * (C + PAD) + s] = s <= t ? a.scale * dp[i][j] * lin_exp2(G[t] - G[s]) : 0.f;
+            const float zz = s <= t ? pv[i][j] * dp[i][j] : 0.f;
+            z += zz;
+            zcol[j] += zz;
+        }
+        z = row_sum(z);
+        const float fa = a.scale * lin_exp2(G[t]), fw = lin_exp2(G[C - 1] - G[t]);
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            dqi[i][j] *= fa;
+            dki[i][j] *= fw;
+            x = fmaf(dqi[i][j], Qs[t * (DK + PAD) + tx + 16 * j], x);
+            y = fmaf(dki[i][j], Ks[t * (DK + PAD) + tx + 16 * j], y);
+        }
+        x = row_sum(x);
+        y = row_sum(y);
+        if (tx == 0) { zr[t] = z; xi[t] = x; yi[t] = y; }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float z = zcol[j] + __shfl_xor_sync(0xffffffffu, zcol[j], 16);
+        if (lane < 16) zc[warp][tx + 16 * j] = z;
+    }
+    sr = warp_sum(sr);
+    if (lane == 0) wsum[warp] = sr;
+    __syncthreads();
+
+    mm<NK, false, false>(dqi, As, C + PAD, Ks, DK + PAD, C, ty, tx);
+    mm<NK, true, false>(dki, As, C + PAD, Qs, DK + PAD, C, ty, tx);
+    Tin *dq = static_cast<Tin *>(b.dq) + ((size_t)tok * a.H + h) * DK, *dk = static_cast<Tin *>(b.dk) + ((size_t)tok * a.H + h) * DK;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = ty * 4 + i;
+        if (t >= L) continue;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            stf(dq + (size_t)t * a.H * DK + tx + 16 * j, dqi[i][j]);
+            stf(dk + (size_t)t * a.H * DK + tx + 16 * j, dki[i][j]);
+        }
+    }
+    if (b.dg && warp == 0) {   // two tokens per lane, sums over the tokens from t on and before t in fp64
+        float s0 = 0.f;
+        for (int w = 0; w < 8; ++w) s0 += wsum[w];
+        const double whole = (double)lin_exp2(G[C - 1]) * s0;
+        double later[2], earlier[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            float z = 0.f;
+            for (int w = 0; w < 8; ++w) z += zc[w][t];
+            later[e] = (double)zr[t] - z + xi[t];
+            earlier[e] = yi[t];
+        }
+        double sl = later[0] + later[1], se = earlier[0] + earlier[1];
+        double fl = sl, fe = se;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const double yl = __shfl_down_sync(0xffffffffu, fl, off), ye = __shfl_up_sync(0xffffffffu, fe, off);
+            if (lane + off < 32) fl += yl;
+            if (lane >= off) fe += ye;
+        }
+        fl -= sl;              // tokens of the lanes above
+        fe -= se;              // tokens of the lanes below
+        const double d1 = whole + fl + later[1] + fe + earlier[0], d0 = whole + fl + later[1] + later[0] + fe;
+        if (a.decay == KDN_DECAY_TOKEN) {
+            if (2 * lane < L) b.dg[(size_t)(tok + 2 * lane) * a.H + h] = (float)d0;
+            if (2 * lane + 1 < L) b.dg[(size_t)(tok + 2 * lane + 1) * a.H + h] = (float)d1;
+        } else {
+            double d = (2 * lane < L ? d0 : 0.0) + (2 * lane + 1 < L ? d1 : 0.0);
+            for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+            if (lane == 0) ws.dgc[(size_t)u * a.H + h] = (float)d;
+        }
+    }
+}
+
+// dg[h] of a per-head decay: the chunks' shares in a fixed order
+__global__ void __launch_bounds__(256) linear_head_decay_kernel(LinArgs a, const float *dgc, float *dg, int slots, int tokens)
+{
+    __shared__ double part[256];
+    const int h = blockIdx.x;
+    double s = 0.0;
+    for (int u = threadIdx.x; u < slots; u += 256) {
+        LinPiece p;
+        if (lin_piece(a, u, tokens, p) && p.len > 0) s += dgc[(size_t)u * a.H + h];
+    }
+    part[threadIdx.x] = s;
+    __syncthreads();
+    for (int off = 128; off > 0; off >>= 1) {
+        if ((int)threadIdx.x < off) part[threadIdx.x] += part[threadIdx.x + off];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) dg[h] = (float)part[0];
+}
+
+// ------------------------------------------------------------------ host side
+namespace {
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+long long slots_of(const LinArgs &a) { return lin_slots(a.cu != nullptr, a.T, a.ntok, a.nseq, C); }
+size_t state_bytes(const LinArgs &a) { return round256((size_t)slots_of(a) * a.H * a.dk * a.dv * 4); }
+size_t head_bytes(const LinArgs &a) { return round256((size_t)slots_of(a) * a.H * 8); }
+
+template <int DK, int DVT, typename Tin, bool REV>
+cudaError_t delta(const LinArgs &a, const void *X, const void *Y, float *out, float2 *dec, cudaStream_t st) {
+    constexpr size_t smem = sizeof(float) * C * (DK + DVT + 2 * PAD);
+    KernelSetup ks;
+    auto kern = linear_delta_kernel<DK, DVT, Tin, REV>;
+    cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT), NT, smem, st>>>(a, X, Y, out, dec);
+    return cudaGetLastError();
+}
+template <bool REV>
+cudaError_t scan(const LinArgs &a, float *U, const float2 *dec, const float *first, float *last, cudaStream_t st) {
+    const long long threads = (long long)a.nseq * a.H * (a.dk * a.dv / 4);
+    linear_scan_kernel<REV><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, U, dec, first, last);
+    return cudaGetLastError();
+}
+
+template <int DK, int DVT, typename Tin>
+cudaError_t forward(const LinArgs &a, uint8_t *ws, cudaStream_t st) {
+    float *U = reinterpret_cast<float *>(ws);
+    float2 *dec = reinterpret_cast<float2 *>(ws + state_bytes(a));
+    cudaError_t e = delta<DK, DVT, Tin, false>(a, a.k, a.v, U, dec, st);
+    if (e != cudaSuccess) return e;
+    e = scan<false>(a, U, dec, a.S0, a.S_out, st);
+    if (e != cudaSuccess) return e;
+    constexpr size_t smem = sizeof(float) * (C * (2 * DK + DVT + C + 4 * PAD) + DK * (DVT + PAD));
+    KernelSetup ks;
+    auto kern = linear_out_kernel<DK, DVT, Tin>;
+    e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT), NT, smem, st>>>(a, U);
+    return cudaGetLastError();
+}
+
+template <int DK, int DVT, typename Tin>
+cudaError_t backward(const LinBwdArgs &b, uint8_t *wsp, cudaStream_t st) {
+    const LinArgs &a = b.a;
+    Ws ws;
+    ws.U = reinterpret_cast<float *>(wsp);
+    ws.E = reinterpret_cast<float *>(wsp + state_bytes(a));
+    ws.dec = reinterpret_cast<float2 *>(wsp + 2 * state_bytes(a));
+    ws.dgc = reinterpret_cast<float *>(wsp + 2 * state_bytes(a) + head_bytes(a));
+    cudaError_t e = delta<DK, DVT, Tin, false>(a, a.k, a.v, ws.U, ws.dec, st);
+    if (e == cudaSuccess) e = scan<false>(a, ws.U, ws.dec, a.S0, nullptr, st);
+    if (e == cudaSuccess) e = delta<DK, DVT, Tin, true>(a, a.q, b.d_o, ws.E, ws.dec, st);
+    if (e == cudaSuccess) e = scan<true>(a, ws.E, ws.dec, b.dS_T, b.dS0, st);
+    if (e != cudaSuccess) return e;
+    constexpr size_t smem = sizeof(float) * (C * (2 * DK + 2 * DVT + 2 * C + 6 * PAD) + 2 * DK * (DVT + PAD));
+    KernelSetup ks;
+    auto kern = linear_grad_kernel<DK, DVT, Tin>;
+    e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(slots_of(a) * a.H), NT, smem, st>>>(b, ws);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !b.dg || a.decay != KDN_DECAY_HEAD) return e;
+    linear_head_decay_kernel<<<a.H, 256, 0, st>>>(a, ws.dgc, b.dg, (int)slots_of(a), C);
+    return cudaGetLastError();
+}
+
+#define KDN_LINEAR_SIZES(FN, ARG)                                                                              \
+    if (a.dv == 32) {                                                                                          \
+        if (a.dk == 32) return bf16_in ? FN<32, 32, bf16>(ARG, w, st) : FN<32, 32, float>(ARG, w, st);         \
+        if (a.dk == 64) return bf16_in ? FN<64, 32, bf16>(ARG, w, st) : FN<64, 32, float>(ARG, w, st);         \
+        return bf16_in ? FN<128, 32, bf16>(ARG, w, st) : FN<128, 32, float>(ARG, w, st);                       \
+    }                                                                                                          \
+    if (a.dk == 32) return bf16_in ? FN<32, 64, bf16>(ARG, w, st) : FN<32, 64, float>(ARG, w, st);             \
+    if (a.dk == 64) return bf16_in ? FN<64, 64, bf16>(ARG, w, st) : FN<64, 64, float>(ARG, w, st);             \
+    return bf16_in ? FN<128, 64, bf16>(ARG, w, st) : FN<128, 64, float>(ARG, w, st);
+
+}  // namespace
+
+size_t linear_simt_workspace_bytes(const LinArgs &a) { return state_bytes(a) + head_bytes(a); }
+size_t linear_simt_backward_workspace_bytes(const LinArgs &a) { return 2 * state_bytes(a) + 2 * head_bytes(a); }
+
+cudaError_t launch_linear_simt(const LinArgs &a, bool bf16_in, void *workspace, cudaStream_t st) {
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    KDN_LINEAR_SIZES(forward, a)
+}
+cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, bool bf16_in, void *workspace, cudaStream_t st) {
+    const LinArgs &a = b.a;
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    KDN_LINEAR_SIZES(backward, b)
+}
+
+}  // namespace kdn
