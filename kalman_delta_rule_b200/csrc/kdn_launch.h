@@ -76,6 +76,9 @@ size_t linear_simt_workspace_bytes(const LinArgs &a);
 size_t linear_simt_backward_workspace_bytes(const LinArgs &a);
 cudaError_t launch_linear_simt(const LinArgs &a, bool bf16_in, void *workspace, cudaStream_t st);
 cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, bool bf16_in, void *workspace, cudaStream_t st);
+// tensor-core path in chunks of 128 tokens (bf16 inputs)
+size_t linear_tc_workspace_bytes(const LinArgs &a);
+cudaError_t launch_linear_tc(const LinArgs &a, void *workspace, cudaStream_t st);
 // n tokens of N sequences on a state updated in place
 cudaError_t launch_linear_decode(const LinArgs &a, bool bf16_in, cudaStream_t st);
 

@@ -46,6 +46,13 @@ kdn_status_t check_problem(const kdn_linear_problem_t *p, kdn::LinArgs *a) {
     return KDN_OK;
 }
 
+bool on_tensor_cores(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
+    return p->in_dtype == KDN_DTYPE_BF16 && a.ntok > 0;
+}
+size_t forward_bytes(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
+    return on_tensor_cores(p, a) ? kdn::linear_tc_workspace_bytes(a) : kdn::linear_simt_workspace_bytes(a);
+}
+
 kdn_status_t check_norm(long long n, int G, int d, kdn_dtype_t dtype, float eps) {
     if (n < 0 || G <= 0 || d <= 0 || !(eps >= 0.f) || !isfinite(eps)) return KDN_ERR_INVALID_ARG;
     if (dtype != KDN_DTYPE_F32 && dtype != KDN_DTYPE_BF16) return KDN_ERR_INVALID_ARG;
@@ -62,7 +69,7 @@ kdn_status_t kdn_linear_workspace_size(const kdn_linear_problem_t *p, size_t *by
     const kdn_status_t st = check_problem(p, &a);
     if (st != KDN_OK) return st;
     if (!bytes) return KDN_ERR_INVALID_ARG;
-    *bytes = kdn::linear_simt_workspace_bytes(a);
+    *bytes = forward_bytes(p, a);
     return KDN_OK;
 }
 
@@ -76,11 +83,13 @@ kdn_status_t kdn_linear_forward(const kdn_linear_problem_t *p, const void *q, co
     if (a.ntok > 0 && (!q || !k || !v || !o || (a.decay != KDN_DECAY_NONE && !g))) return KDN_ERR_INVALID_ARG;
     if (!aligned({q, k, v, g, S0, o, S_out})) return KDN_ERR_INVALID_ARG;
     if (S_out && S_out == S0) return KDN_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < kdn::linear_simt_workspace_bytes(a) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-        return KDN_ERR_WORKSPACE;
+    const size_t need = forward_bytes(p, a);
+    if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return KDN_ERR_WORKSPACE;
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0; a.o = o; a.S_out = S_out;
     a.err = kdn::error_word();
-    return cuda_status(kdn::launch_linear_simt(a, p->in_dtype == KDN_DTYPE_BF16, workspace, static_cast<cudaStream_t>(stream)));
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (on_tensor_cores(p, a)) return cuda_status(kdn::launch_linear_tc(a, workspace, cs));
+    return cuda_status(kdn::launch_linear_simt(a, p->in_dtype == KDN_DTYPE_BF16, workspace, cs));
 }
 
 kdn_status_t kdn_linear_decode_tokens(int N, int n_tokens, int H, int d_k, int d_v, kdn_dtype_t in_dtype, float scale,
