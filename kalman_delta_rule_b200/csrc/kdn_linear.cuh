@@ -5,8 +5,7 @@
 // recurrence unrolls to
 //     O  = scale ((Q K^T o D) V + diag(e^G) Q S),   D_ts = e^{G_t - G_s} for t >= s, else 0
 //     S' = e^{G_C} S + K^T diag(e^{G_C - G}) V
-// Every factor that the kernels form from a difference of G is at most one (for g <= 0).  G is
-// summed in fp64: a difference of two partial sums of a strongly decaying chunk keeps its bits.
+// Every factor that the kernels form from a difference of G is at most one (for g <= 0).
 #pragma once
 
 #include "kdn_common.cuh"
@@ -79,27 +78,42 @@ __device__ __forceinline__ bool lin_piece(const LinArgs &a, int u, int L, LinPie
     return p.j == 0 || (p.j > 0 && (long long)p.j * L < p.len);
 }
 
-// log2 of a token's decay factor in fp64.  Below 2^-4096 (a reset, g = -inf, included) every fp32
-// factor across the token is 0 either way; the floor keeps differences of sums free of inf - inf.
-__device__ __forceinline__ double lin_log2_decay(const LinArgs &a, int t, int h) {
-    if (a.decay == KDN_DECAY_NONE) return 0.0;
-    const float g = a.decay == KDN_DECAY_HEAD ? __ldg(a.g + h) : __ldg(a.g + (size_t)t * a.H + h);
-    const double x = (double)g * 1.4426950408889634;
-    return x < -4096.0 ? -4096.0 : x;     // a NaN stays a NaN
+// Sums of log2 decays are kept in two floats (about 48 bits): a constant decay near one leaves its mark only
+// after thousands of tokens, and a strongly decaying chunk must not cost two neighbours' difference its bits.
+// (fp64 or 64-bit integers would do too, but take ten times as long: the GPU has few units for them.)  Below
+// e^-2839 (a reset, g = -inf, included) every fp32 factor across a token is 0 either way; the floor keeps
+// differences of sums free of inf - inf.
+struct Log2 {
+    float hi, lo;
+};
+__device__ __forceinline__ Log2 lin_log2(float g) {          // from the natural logarithm; a NaN gives -2839, see the callers
+    const float x = fmaxf(g, -2839.f);
+    const float hi = x * 1.44269504f;
+    return {hi, fmaf(x, 1.44269504f, -hi) + x * 1.92596299e-8f};
 }
-// 2^x for x <= 0; the fp64 argument is split so that its fraction keeps fp32's relative accuracy
-__device__ __forceinline__ float lin_exp2(double x) {
-    const float hi = (float)x;
-    return exp2f(hi) * (1.f + 0.693147180559945f * (float)(x - (double)hi));
+__device__ __forceinline__ Log2 operator+(Log2 a, Log2 b) {   // (Knuth's two-sum, then renormalised)
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+    const float hi = s + e;
+    return {hi, e - (hi - s)};
 }
-
-// A whole chunk's decay 2^x in two floats.  One float would be off by up to half a unit in the last
-// place, the same way in every chunk of a constant decay: over the thousands of chunks of a long memory
-// that adds up to several 1e-6 of the state.
-__device__ __forceinline__ float2 lin_chunk_decay(double x) {
-    const double f = exp2(x);
-    const float hi = (float)f;
-    return make_float2(hi, (float)(f - (double)hi));
+__device__ __forceinline__ Log2 operator-(Log2 a, Log2 b) { return a + Log2{-b.hi, -b.lo}; }
+__device__ __forceinline__ float lin_load_decay(const LinArgs &a, int t, int h) {
+    if (a.decay == KDN_DECAY_NONE) return 0.f;
+    return a.decay == KDN_DECAY_HEAD ? __ldg(a.g + h) : __ldg(a.g + (size_t)t * a.H + h);
+}
+__device__ __forceinline__ float lin_exp2(Log2 x) { return exp2f(x.hi) * fmaf(x.lo, 0.693147181f, 1.f); }
+// 2^(a - b); the difference is rounded to fp32, an error of 2^-24 of the exponent (where that is large the factor is tiny)
+__device__ __forceinline__ float lin_exp2_between(Log2 a, Log2 b) { return exp2f((a.hi - b.hi) + (a.lo - b.lo)); }
+// A whole chunk's decay 2^x in two floats, 1 + expm1.  One float would be off by up to half a unit in the
+// last place, the same way in every chunk of a constant decay: over the chunks that a decay near one lets
+// the memory last that adds up to several 1e-6 of the state.  What is left is relative to 1 - 2^x.  Below
+// one half, where nothing lasts, one float and its exponential do (1 + expm1 would cancel).
+__device__ __forceinline__ float2 lin_chunk_decay(Log2 x) {
+    if (x.hi < -1.f) return make_float2(lin_exp2(x), 0.f);
+    const float z = expm1f(fmaf(x.hi, 0.693147181f, fmaf(x.hi, -1.90465421e-9f, x.lo * 0.693147181f)));
+    const float hi = 1.f + z;
+    return make_float2(hi, z - (hi - 1.f));
 }
 __device__ __forceinline__ float lin_carry(float2 decay, float s, float u) { return fmaf(decay.x, s, fmaf(decay.y, s, u)); }
 

@@ -78,25 +78,34 @@ __device__ __forceinline__ void load_state(float *dst, const float *src, int dv)
     }
 }
 
-// G (log2, inclusive) of the chunk's C tokens to shared memory by warp 0; decay 1 behind the end
-__device__ __forceinline__ void chunk_log_decay(const LinArgs &a, int tok, int L, int h, double *G) {
+// G (log2, inclusive) of the chunk's C tokens to shared memory by warp 0; decay 1 behind the end.  A NaN
+// among the log decays is put where every factor of the chunk meets it.
+struct ChunkDecay {
+    Log2 G[C];
+    float one;                 // 1, or NaN
+};
+__device__ __forceinline__ void chunk_log_decay(const LinArgs &a, int tok, int L, int h, ChunkDecay *d) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        double x0 = 2 * lane < L ? lin_log2_decay(a, tok + 2 * lane, h) : 0.0;
-        double x1 = x0 + (2 * lane + 1 < L ? lin_log2_decay(a, tok + 2 * lane + 1, h) : 0.0);
-        double s = x1;
+        float g[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) g[i] = 2 * lane + i < L ? lin_load_decay(a, tok + 2 * lane + i, h) : 0.f;
+        const bool bad = __any_sync(0xffffffffu, g[0] != g[0] || g[1] != g[1]);
+        const Log2 x0 = lin_log2(g[0]), x1 = x0 + lin_log2(g[1]);
+        Log2 s = x1;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, s, off);
-            if (lane >= off) s += y;
+            const Log2 y = {__shfl_up_sync(0xffffffffu, s.hi, off), __shfl_up_sync(0xffffffffu, s.lo, off)};
+            if (lane >= off) s = y + s;
         }
-        const double before = s - x1;
-        G[2 * lane] = before + x0;
-        G[2 * lane + 1] = s;
+        Log2 before = {__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};
+        if (lane == 0) before = {0.f, 0.f};
+        d->G[2 * lane] = before + x0;
+        d->G[2 * lane + 1] = s;
+        if (lane == 0) d->one = bad ? __int_as_float(0x7fc00000) : 1.f;
     }
     __syncthreads();
 }
-
 // sum over the 16 threads of a row (lanes tx = 0..15)
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
@@ -118,20 +127,24 @@ __global__ void __launch_bounds__(NT) linear_delta_kernel(LinArgs a, const void 
 {
     extern __shared__ __align__(16) float sm[];
     float *Xs = sm, *Ys = sm + C * (DK + PAD);
-    __shared__ double G[C];
+    __shared__ ChunkDecay dec_s;
+    const Log2 *G = dec_s.G;
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H, col = blockIdx.y * DVT;
     LinPiece p;
     if (!lin_piece(a, u, C, p) || p.len == 0) return;
     const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
     load_rows<DK, Tin>(Xs, X, tok, L, a.H, h, DK, 0);
     load_rows<DVT, Tin>(Ys, Y, tok, L, a.H, h, a.dv, col);
-    chunk_log_decay(a, tok, L, h, G);
+    chunk_log_decay(a, tok, L, h, &dec_s);
     for (int i = threadIdx.x; i < L * (DVT / 4); i += NT) {
         const int r = i / (DVT / 4);
         float4 *y = reinterpret_cast<float4 *>(Ys + r * (DVT + PAD) + (i % (DVT / 4)) * 4);
-        *y = scale4(*y, REV ? a.scale * lin_exp2(G[r]) : lin_exp2(G[C - 1] - G[r]));
+        *y = scale4(*y, dec_s.one * (REV ? a.scale * lin_exp2(G[r]) : lin_exp2_between(G[C - 1], G[r])));
     }
-    if (blockIdx.y == 0 && threadIdx.x == 0) dec[(size_t)u * a.H + h] = lin_chunk_decay(G[C - 1]);
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        const float2 f = lin_chunk_decay(G[C - 1]);
+        dec[(size_t)u * a.H + h] = make_float2(f.x * dec_s.one, f.y);
+    }
     __syncthreads();
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     float *dst = out + ((size_t)u * a.H + h) * DK * a.dv + col;
@@ -198,7 +211,8 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
     extern __shared__ __align__(16) float sm[];
     float *Qs = sm, *Ks = Qs + C * (DK + PAD), *Vs = Ks + C * (DK + PAD), *Ss = Vs + C * (DVT + PAD),
           *Ps = Ss + DK * (DVT + PAD);
-    __shared__ double G[C];
+    __shared__ ChunkDecay dec_s;
+    const Log2 *G = dec_s.G;
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H, col = blockIdx.y * DVT;
     LinPiece p;
     if (!lin_piece(a, u, C, p) || p.len == 0) return;
@@ -207,7 +221,8 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
     load_rows<DK, Tin>(Ks, a.k, tok, L, a.H, h, DK, 0);
     load_rows<DVT, Tin>(Vs, a.v, tok, L, a.H, h, a.dv, col);
     load_state<DK, DVT>(Ss, S + ((size_t)u * a.H + h) * DK * a.dv + col, a.dv);
-    chunk_log_decay(a, tok, L, h, G);
+    chunk_log_decay(a, tok, L, h, &dec_s);
+    const float scale = a.scale * dec_s.one;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     {
         float acc[4][4] = {};
@@ -217,7 +232,7 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = ty * 4 + i, s = tx + 16 * j;
-                Ps[t * (C + PAD) + s] = s <= t ? a.scale * acc[i][j] * lin_exp2(G[t] - G[s]) : 0.f;
+                Ps[t * (C + PAD) + s] = s <= t ? scale * acc[i][j] * lin_exp2_between(G[t], G[s]) : 0.f;
             }
     }
     __syncthreads();
@@ -225,7 +240,7 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
     mm<DVT / 16, false, false>(acc, Qs, DK + PAD, Ss, DVT + PAD, DK, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float f = a.scale * lin_exp2(G[ty * 4 + i]);
+        const float f = scale * lin_exp2(G[ty * 4 + i]);
 #pragma unroll
         for (int j = 0; j < DVT / 16; ++j) acc[i][j] *= f;
     }
@@ -255,7 +270,8 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
     extern __shared__ __align__(16) float sm[];
     float *Qs = sm, *Ks = Qs + C * (DK + PAD), *Vs = Ks + C * (DK + PAD), *Os = Vs + C * (DVT + PAD),
           *Ss = Os + C * (DVT + PAD), *Rs = Ss + DK * (DVT + PAD), *Ps = Rs + DK * (DVT + PAD), *As = Ps + C * (C + PAD);
-    __shared__ double G[C];
+    __shared__ ChunkDecay dec_s;
+    const Log2 *G = dec_s.G;
     __shared__ float zr[C], zc[8][C], xi[C], yi[C], wsum[8];
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H;
     LinPiece p;
@@ -265,8 +281,9 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
     const size_t sbase = ((size_t)u * a.H + h) * DK * a.dv;
     load_rows<DK, Tin>(Qs, a.q, tok, L, a.H, h, DK, 0);
     load_rows<DK, Tin>(Ks, a.k, tok, L, a.H, h, DK, 0);
-    chunk_log_decay(a, tok, L, h, G);
+    chunk_log_decay(a, tok, L, h, &dec_s);
 
+    const float scale = a.scale * dec_s.one;
     float pv[4][4] = {};
     mm<4, false, true>(pv, Qs, DK + PAD, Ks, DK + PAD, DK, ty, tx);
 #pragma unroll
@@ -274,7 +291,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int t = ty * 4 + i, s = tx + 16 * j;
-            pv[i][j] = s <= t ? a.scale * pv[i][j] * lin_exp2(G[t] - G[s]) : 0.f;
+            pv[i][j] = s <= t ? scale * pv[i][j] * lin_exp2_between(G[t], G[s]) : 0.f;
             Ps[t * (C + PAD) + s] = pv[i][j];
         }
 
@@ -298,7 +315,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
         mm<NV, false, false>(acc, Ks, DK + PAD, Rs, DVT + PAD, DK, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float w = lin_exp2(G[C - 1] - G[ty * 4 + i]);
+            const float w = lin_exp2_between(G[C - 1], G[ty * 4 + i]);
 #pragma unroll
             for (int j = 0; j < NV; ++j) acc[i][j] *= w;
         }
@@ -322,13 +339,13 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int s = tx + 16 * j;
-            As[t * (C + PAD) + s] = s <= t ? a.scale * dp[i][j] * lin_exp2(G[t] - G[s]) : 0.f;
+            As[t * (C + PAD) + s] = s <= t ? scale * dp[i][j] * lin_exp2_between(G[t], G[s]) : 0.f;
             const float zz = s <= t ? pv[i][j] * dp[i][j] : 0.f;
             z += zz;
             zcol[j] += zz;
         }
         z = row_sum(z);
-        const float fa = a.scale * lin_exp2(G[t]), fw = lin_exp2(G[C - 1] - G[t]);
+        const float fa = scale * lin_exp2(G[t]), fw = lin_exp2_between(G[C - 1], G[t]);
         float x = 0.f, y = 0.f;
 #pragma unroll
         for (int j = 0; j < NK; ++j) {

@@ -6,12 +6,10 @@
 // Forward (linear_forward_kernel): a CTA walks one segment of a sequence for one head and 64 columns of
 // d_v, chunk by chunk, with everything but the inputs and outputs on chip.  Warp roles, each a loop over
 // the chunks that meets the others at mbarriers:
-//   TMA      loads Q, K and the V tile of chunk c + 2 as soon as chunk c's MMAs have read theirs
-//   decay    sums the log decays of chunk c + 1, forms its factors
-//   MMA      one thread: OS = Q S, delta = K^T V', OI = P V (P from TMEM), scores of c + 1 = Q K^T
-//   A (8)    scores (TMEM) -> decayed, masked, bf16 -> P (TMEM, in place); o = scale (OI + e^G OS)
-//   B (8)    V' = diag(e^{G_C - G}) V as three bf16 terms; S <- e^{G_C} S + delta in registers (fp32),
-//            its bf16 copy for the next Q S
+//   TMA      refills Q, K, the V tile and the decay record for chunk c + 2, each as soon as chunk c is done with it
+//   MMA      one thread: scores = Q K^T, delta = K^T V', OS = Q S, OI = P V (P from TMEM)
+//   W (8)    V' = diag(e^{G_C - G}) V as three bf16 terms; scores (TMEM) -> decayed, masked, bf16 -> P (TMEM)
+//   S (8)    S <- e^{G_C} S + delta in registers (fp32), its bf16 copy for Q S; o = scale (OI + e^G OS)
 // What bounds it is one pass over q, k, v and o at HBM's rate; the MMAs take about 2050 cycles per chunk
 // and tile (scores 512, Q S 384, delta 896 -- its A operand is read from shared memory three times --,
 // P V 256), which is about what the chunk's bytes take at an SM's share of the bandwidth.
@@ -32,19 +30,20 @@ using namespace lin;
 
 namespace {
 
-constexpr int NW_A = 8, NW_B = 8;                     // epilogue warps
-constexpr int NT_F = (NW_A + NW_B + 3) * 32;          // and the TMA, MMA and decay warps
+// warps: W weighted rows (forward: and scores), S state (forward: and outputs); then MMA and TMA
+constexpr int NW_W = 8, NW_S = 8;
+constexpr int NT_F = (NW_W + NW_S + 2) * 32;
+constexpr int NT_S = (NW_W + NW_S + 2) * 32;
 
 struct FwdSmem {
     static constexpr int Q = 0, K = Q + 2 * 2 * ATOM, V = K + 2 * 2 * ATOM, VP = V + 2 * ATOM, S = VP + 3 * ATOM,
-                         DEC = S + ATOM, META = DEC + 2 * (int)sizeof(Decay), BAR = META + 2 * (int)sizeof(DecayMeta),
-                         NBAR = 17, CTL = BAR + NBAR * 8, TOTAL = CTL + 16;
+                         DEC = S + ATOM, BAR = DEC + 2 * (int)sizeof(Decay), NBAR = 22, CTL = BAR + NBAR * 8, TOTAL = CTL + 16;
 };
 static_assert(FwdSmem::TOTAL <= 227 * 1024, "shared memory");
 
 struct StateSmem {
     static constexpr int X = 0, Y = X + 2 * 2 * ATOM, VP = Y + 2 * ATOM, DEC = VP + 2 * 3 * ATOM,
-                         META = DEC + 2 * (int)sizeof(Decay), BAR = META + 2 * (int)sizeof(DecayMeta), NBAR = 14,
+                         BAR = DEC + 2 * (int)sizeof(Decay), NBAR = 14,
                          CTL = BAR + NBAR * 8, TOTAL = CTL + 16;
 };
 static_assert(StateSmem::TOTAL <= 227 * 1024, "shared memory");
@@ -59,6 +58,7 @@ struct Split {
 struct FwdArgs {
     LinArgs a;
     Split sp;
+    const Decay *decay;            // [slots of C][H]
     CUtensorMap tq, tk, tv;
 };
 
@@ -70,59 +70,56 @@ struct StateArgs {
     float *last;                   // STATES: state behind the last (REV: gradient before the first) chunk, or NULL
     float *tiles;                  // TOTALS: [slots of sub]; STATES: [slots of C][H][tiles]
     float2 *dec;                   // TOTALS
+    const Decay *decay;            // [slots of C][H]
     CUtensorMap tx, ty;
 };
 
-// 32 columns of row `row` of a state: from the caller's [dk, dv] layout (zero outside it) ...
-__device__ __forceinline__ void load_caller(float (&S)[32], const float *src, int dk, int dv, int row, int col) {
+// 32 columns of row `row` of a state, in pairs: from the caller's [dk, dv] layout (zero outside it) ...
+__device__ __forceinline__ void load_caller(f32x2 (&S)[16], const float *src, int dk, int dv, int row, int col) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const float4 x = src && row < dk && col < dv ? __ldg(reinterpret_cast<const float4 *>(src + (size_t)row * dv + col + j))
+    for (int j = 0; j < 8; ++j) {
+        const float4 x = src && row < dk && col < dv ? __ldg(reinterpret_cast<const float4 *>(src + (size_t)row * dv + col) + j)
                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-        S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+        S[2 * j] = pk2(x.x, x.y);
+        S[2 * j + 1] = pk2(x.z, x.w);
     }
 }
-__device__ __forceinline__ void store_caller(const float (&S)[32], float *dst, int dk, int dv, int row, int col) {
+__device__ __forceinline__ float4 quad(const f32x2 (&S)[16], int j) { return make_float4(x2(S[2 * j]), y2(S[2 * j]), x2(S[2 * j + 1]), y2(S[2 * j + 1])); }
+__device__ __forceinline__ void store_caller(const f32x2 (&S)[16], float *dst, int dk, int dv, int row, int col) {
     if (row >= dk || col >= dv) return;
 #pragma unroll
-    for (int j = 0; j < 32; j += 4)
-        *reinterpret_cast<float4 *>(dst + (size_t)row * dv + col + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+    for (int j = 0; j < 8; ++j) *(reinterpret_cast<float4 *>(dst + (size_t)row * dv + col) + j) = quad(S, j);
 }
 // ... and to a workspace tile
-__device__ __forceinline__ void store_tile(const float (&S)[32], float *tile, int row, int half) {
+__device__ __forceinline__ void store_tile(const f32x2 (&S)[16], float *tile, int row, int half) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<float4 *>(tile + ((half * 8 + q) * 128 + row) * 4) = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+    for (int j = 0; j < 8; ++j) *reinterpret_cast<float4 *>(tile + ((half * 8 + j) * 128 + row) * 4) = quad(S, j);
 }
-// S <- decay S + the tile of a sub-segment
-__device__ __forceinline__ void fold_tile(float (&S)[32], const float *tile, float2 dec, int row, int half) {
+// S <- decay S + x: the decay in two floats (see lin_chunk_decay)
+__device__ __forceinline__ f32x2 carry2(f32x2 hi, f32x2 lo, f32x2 s, f32x2 x) { return fma2(hi, s, fma2(lo, s, x)); }
+// ... with the tile of a sub-segment
+__device__ __forceinline__ void fold_tile(f32x2 (&S)[16], const float *tile, float2 dec, int row, int half) {
+    const f32x2 hi = pk2(dec.x, dec.x), lo = pk2(dec.y, dec.y);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(tile + ((half * 8 + q) * 128 + row) * 4));
-        S[4 * q] = lin_carry(dec, S[4 * q], x.x);
-        S[4 * q + 1] = lin_carry(dec, S[4 * q + 1], x.y);
-        S[4 * q + 2] = lin_carry(dec, S[4 * q + 2], x.z);
-        S[4 * q + 3] = lin_carry(dec, S[4 * q + 3], x.w);
+    for (int j = 0; j < 8; ++j) {
+        const float4 x = __ldg(reinterpret_cast<const float4 *>(tile + ((half * 8 + j) * 128 + row) * 4));
+        S[2 * j] = carry2(hi, lo, S[2 * j], pk2(x.x, x.y));
+        S[2 * j + 1] = carry2(hi, lo, S[2 * j + 1], pk2(x.z, x.w));
     }
 }
-__device__ __forceinline__ void add_delta(float (&S)[32], uint32_t d, float2 dec) {
+// ... with a chunk's delta from TMEM
+__device__ __forceinline__ void add_delta(f32x2 (&S)[16], uint32_t d, float2 dec) {
+    const f32x2 hi = pk2(dec.x, dec.x), lo = pk2(dec.y, dec.y);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        float x[16], y[16];
-        tmem_ld16(d + p * 16, x);
-        tmem_ld16(d + 64 + p * 16, y);
+    for (int p = 0; p < 4; ++p) {
+        float x[8], y[8], z[8];
+        tmem_ld8x3(d + p * 8, d + 64 + p * 8, d + 128 + p * 8, x, y, z);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) S[p * 16 + j] = lin_carry(dec, S[p * 16 + j], x[j] + y[j]);
+        for (int j = 0; j < 4; ++j) {
+            const f32x2 low = add2(pk2(y[2 * j], y[2 * j + 1]), pk2(z[2 * j], z[2 * j + 1]));
+            S[p * 4 + j] = carry2(hi, lo, S[p * 4 + j], add2(pk2(x[2 * j], x[2 * j + 1]), low));
+        }
     }
-}
-
-// meeting of the two warps of a quadrant: whether both came with `ok`, the same answer for both (a warp
-// whose wait gave up still comes, so that the other is not left behind)
-__device__ __forceinline__ bool both(int id, bool ok) {
-    int r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, %2, 64, p;\n selp.b32 %0, 1, 0, q;\n}"
-                 : "=r"(r) : "r"((int)ok), "r"(id) : "memory");
-    return r != 0;
 }
 
 // thread 0 of the TMA warp: a [128 tokens][64 channels] tile as two boxes of 64 tokens
@@ -136,7 +133,63 @@ __device__ __noinline__ void drain(uint64_t *bar, uint32_t parity) { mbar_wait(b
 
 }  // namespace
 
+// ================================================================= decay records
+// a warp per (chunk, head), four tokens per lane
+__global__ void __launch_bounds__(256) linear_decay_kernel(LinArgs a, Decay *rec, long long n)
+{
+    const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (id >= n) return;
+    const int u = (int)(id / a.H), h = (int)(id % a.H);
+    LinPiece p;
+    if (!lin_piece(a, u, C, p) || p.len == 0) return;
+    const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
+    Decay *d = rec + id;
+    float g[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        g[i] = 0.f;
+        if (lane * 4 + i < L) g[i] = lin_load_decay(a, tok + lane * 4 + i, h);
+    }
+    Log2 G[4];
+    bool bad = false, in = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bad = bad || g[i] != g[i];
+        G[i] = i ? G[i - 1] + lin_log2(g[i]) : lin_log2(g[i]);
+    }
+    Log2 s = G[3];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const Log2 y = {__shfl_up_sync(0xffffffffu, s.hi, off), __shfl_up_sync(0xffffffffu, s.lo, off)};
+        if (lane >= off) s = y + s;
+    }
+    Log2 before = {__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        G[i] = before + G[i];
+        in = in && fabsf(G[i].hi) <= 60.f;
+    }
+    const bool factored = __all_sync(0xffffffffu, in);
+    bad = __any_sync(0xffffffffu, bad);
+    float b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        b[i] = factored ? lin_exp2({-G[i].hi, -G[i].lo}) : G[i].hi;
+        if (bad) b[i] = __int_as_float(0x7fc00000);
+    }
+    *reinterpret_cast<float4 *>(d->b + lane * 4) = make_float4(b[0], b[1], b[2], b[3]);
+    *reinterpret_cast<float4 *>(d->lo + lane * 4) = make_float4(G[0].lo, G[1].lo, G[2].lo, G[3].lo);
+    if (lane == 31) {
+        d->whole = bad ? make_float2(__int_as_float(0x7fc00000), 0.f) : lin_chunk_decay(s);
+        d->total = s;
+        d->factored = factored;
+    }
+}
+
 // ================================================================= forward
+template <int KATOMS>       // 64-channel tiles of q and k in use
 __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_constant__ FwdArgs f)
 {
     using L_ = FwdSmem;
@@ -146,42 +199,46 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
     const int tiles = (a.dv + DVT - 1) / DVT;
     const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % a.H, u = blockIdx.x / tiles / a.H;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int W_S = NW_W, W_MMA = W_S + NW_S, W_TMA = W_MMA + 1;   // MMA beside the rows with the fewest scores
     LinPiece pc;
     if (!lin_piece(a, u, f.sp.seg, pc)) return;
     const int tok0 = pc.t0 + pc.j * f.sp.seg, len = min(f.sp.seg, pc.len - pc.j * f.sp.seg);
     const int n = (len + C - 1) / C;
-    const int katoms = a.dk > 64 ? 2 : 1;
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L_::BAR);
-    uint64_t *full = bar, *empty = bar + 2, *sc_full = bar + 4, *p_full = bar + 6, *dec_full = bar + 8, *dec_empty = bar + 10,
-             *o_full = bar + 12, *o_free = bar + 13, *dl_full = bar + 14, *vp_full = bar + 15, *s_full = bar + 16;
+    uint64_t *qk_full = bar, *v_full = bar + 2, *q_free = bar + 4, *k_free = bar + 6, *v_free = bar + 8, *dec_full = bar + 10,
+             *dec_free = bar + 12, *o_free = bar + 14, *sc_full = bar + 15, *p_full = bar + 16, *o_full = bar + 17,
+             *dl_full = bar + 18, *dl_free = bar + 19, *vp_full = bar + 20, *s_full = bar + 21;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L_::CTL);
     int *abort_flag = reinterpret_cast<int *>(sm + L_::CTL + 4);
     const Waits w{abort_flag};
     Decay *dec = reinterpret_cast<Decay *>(sm + L_::DEC);
-    DecayMeta *meta = reinterpret_cast<DecayMeta *>(sm + L_::META);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, 1);
-            mbar_init(sc_full + i, 1);
-            mbar_init(p_full + i, NW_A);
+            mbar_init(qk_full + i, 1);
+            mbar_init(v_full + i, 1);
+            mbar_init(q_free + i, 1);
+            mbar_init(k_free + i, 1);
+            mbar_init(v_free + i, 1);
             mbar_init(dec_full + i, 1);
-            mbar_init(dec_empty + i, NW_A + NW_B);
+            mbar_init(dec_free + i, NW_W + NW_S);
         }
+        mbar_init(sc_full, 1);
+        mbar_init(p_full, NW_W);
         mbar_init(o_full, 1);
-        mbar_init(o_free, NW_A);
+        mbar_init(o_free, NW_S);
         mbar_init(dl_full, 1);
-        mbar_init(vp_full, NW_B);
-        mbar_init(s_full, NW_B);
+        mbar_init(dl_free, NW_S);
+        mbar_init(vp_full, NW_W);
+        mbar_init(s_full, NW_S);
         mbar_fence_init();
         *abort_flag = (sb & 1023u) ? 1 : 0;   // the swizzled tiles need 1 KB alignment
         tma_prefetch_desc(&f.tq);
         tma_prefetch_desc(&f.tk);
         tma_prefetch_desc(&f.tv);
     }
-    if (katoms == 1) {                        // channels 64..127 of K and Q: zeros, never written again
+    if (KATOMS == 1) {                        // channels 64..127 of K and Q: zeros, never written again
         for (int i = threadIdx.x; i < 4 * (ATOM / 16); i += NT_F) {
             const int t = i / (ATOM / 16);
             *reinterpret_cast<uint4 *>(sm + ((t & 1) ? L_::K : L_::Q) + (t >> 1) * 2 * ATOM + ATOM + (i % (ATOM / 16)) * 16) =
@@ -189,216 +246,191 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
         }
         fence_async_smem();
     }
-    if (warp == NW_A + NW_B + 1) tmem_alloc(tmem_slot, 512);
+    if (warp == W_MMA) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t T_SC = tmem, T_OI = tmem + 256, T_OS = tmem + 320, T_DL = tmem + 384;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const uint32_t T_SC = tmem, T_P = tmem + 128, T_OI = tmem + 192, T_OS = tmem + 256, T_DL = tmem + 320;
     const uint32_t lanes = ((uint32_t)(warp & 3) * 32u) << 16;
     const int row = (warp & 3) * 32 + lane;
 
-    if (warp < NW_A) {
-        // ---------------------------------------------------------- A: scores -> P, and the outputs
+    if (warp < W_S) {
+        // ---------------------------------------------------------- W: weighted rows of V, then the scores
         const int half = warp >> 2, q4 = warp & 3;
-        float since[2];                       // 2^{G_t} of the row, for the chunk's output
-        bool fact[2];
-        auto scores = [&](int c) -> bool {
-            const int st = c & 1;
-            bool ok = w.wait(dec_full + st, (c >> 1) & 1);
+        for (int c = 0; c < n; ++c) {
+            const int st = c & 1, L = min(C, len - c * C);
+            if (!w.wait(dec_full + st, (c >> 1) & 1) || !w.wait(v_full + st, (c >> 1) & 1)) break;
             const Decay &d = dec[st];
-            const bool factored = meta[st].factored;
-            fact[st] = factored;
-            since[st] = decay_since(d, factored, row);
-            ok = ok && w.wait(sc_full + st, (c >> 1) & 1);
+            const bool factored = d.factored;
+            const float until = decay_until(d, row);
+            if (c >= 1 && !w.wait(dl_full, (c - 1) & 1)) break;   // the MMAs that read the weighted rows before
+            if (row < L) {
+                weigh_row(sm + L_::V + st * ATOM, sm + L_::VP, row, half, until);
+            } else {                          // rows behind the sequence's end: zeros in every operand that is summed over rows
+#pragma unroll 1
+                for (int k = 0; k < 3; ++k) zero_row(sm + L_::VP + k * ATOM, row, half * 4, 4);
+                zero_row(sm + L_::V + st * ATOM, row, half * 4, 4);
+                if (w.wait(qk_full + st, (c >> 1) & 1)) zero_row(sm + L_::K + (st * 2 + half) * ATOM, row, 0, 8);
+            }
+            fence_async_smem();
+            warp_arrive(vp_full);
+
+            if (!w.wait(sc_full, c & 1)) break;
             tc_fence_after();
-            // column blocks of 32: this warp takes blocks half and half + 2; blocks above the diagonal are zero
-            uint32_t p[2][16];
+            // P: pieces of 16 columns, every other one is this warp's; zero above the diagonal
+#pragma unroll 1
+            for (int c16 = half * 16; c16 < C; c16 += 32) {
+                uint32_t p[8] = {};
+                if (c16 <= q4 * 32 + 31) {
+                    float x[16];
+                    tmem_ld16(T_SC + lanes + c16, x);
+                    if (factored) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int blk = half + 2 * i;
-                if (blk > q4) {
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 b = *reinterpret_cast<const float4 *>(d.b + c16 + j);
+                            x[j] *= b.x; x[j + 1] *= b.y; x[j + 2] *= b.z; x[j + 3] *= b.w;
+                        }
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) p[i][j] = 0u;
-                    continue;
-                }
-                float x[32];
-                tmem_ld32(T_SC + st * 128 + lanes + blk * 32, x);
-                if (factored) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 b = *reinterpret_cast<const float4 *>(d.b + blk * 32 + j);
-                        x[j] *= b.x; x[j + 1] *= b.y; x[j + 2] *= b.z; x[j + 3] *= b.w;
+                        for (int j = 0; j < 16; ++j) x[j] *= decay_pair(d, row, c16 + j);
                     }
-                } else {
+                    if (c16 + 15 > q4 * 32) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] *= blk * 32 + j <= row ? decay_pair(d, row, blk * 32 + j) : 0.f;
+                        for (int j = 0; j < 16; ++j) x[j] = c16 + j <= row ? x[j] : 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) p[j] = round_bf16x2(pk2(x[2 * j], x[2 * j + 1]));
                 }
-                if (blk == q4) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = j <= lane ? x[j] : 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) p[i][j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+                tmem_st8(T_P + lanes + c16 / 2, p);
             }
-            // P takes the place of the scores' first 64 columns: the quadrant's other warp has read them too
-            if (!both(1 + q4, ok)) return false;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float y[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(p[i][j]);
-                tmem_st16(T_SC + st * 128 + lanes + (half + 2 * i) * 16, y);
-            }
+            tmem_wait_st();
             tc_fence_before();
-            warp_arrive(p_full + st);
-            warp_arrive(dec_empty + st);
-            return true;
-        };
-        auto output = [&](int c) -> bool {
-            const int st = c & 1, L = min(C, len - c * C), col = tile * DVT + half * 32;
-            if (!w.wait(o_full, c & 1)) return false;
-            tc_fence_after();
-            // factored: the row's 2^{G_t} is common to both parts (P holds the columns' 2^{-G_s})
-            const float fs = a.scale * since[st], fi = fact[st] ? fs : a.scale;
-            bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(tok0 + c * C + row) * a.H + h) * a.dv + col;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                float x[16], y[16];
-                tmem_ld16(T_OI + lanes + half * 32 + p * 16, x);
-                tmem_ld16(T_OS + lanes + half * 32 + p * 16, y);
-                if (p == 1) {
-                    tc_fence_before();
-                    warp_arrive(o_free);
-                }
-                if (row < L && col < a.dv) {
-#pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        uint32_t z[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            z[i] = pack_bf16x2(fmaf(fi, x[j + 2 * i], fs * y[j + 2 * i]), fmaf(fi, x[j + 2 * i + 1], fs * y[j + 2 * i + 1]));
-                        *reinterpret_cast<uint4 *>(o + p * 16 + j) = make_uint4(z[0], z[1], z[2], z[3]);
-                    }
-                }
-            }
-            return true;
-        };
-        bool ok = n == 0 || scores(0);
-        for (int c = 0; c < n && ok; ++c) {
-            if (c + 1 < n) ok = scores(c + 1);
-            ok = ok && output(c);
+            warp_arrive(p_full);
+            warp_arrive(dec_free + st);
         }
-    } else if (warp < NW_A + NW_B) {
-        // ---------------------------------------------------------- B: weighted rows of V, the state
-        const int half = (warp - NW_A) >> 2;
-        const int vrow = (threadIdx.x - NW_A * 32) & 127, vhalf = (threadIdx.x - NW_A * 32) >> 7;
+    } else if (warp < W_MMA) {
+        // ---------------------------------------------------------- S: the state, then the outputs
+        const int half = (warp - W_S) >> 2;
         const int col = tile * DVT + half * 32;
         const size_t se = ((size_t)pc.s * a.H + h) * a.dk * a.dv;
-        float S[32];
+        f32x2 S[16];
         load_caller(S, a.S0 ? a.S0 + se : nullptr, a.dk, a.dv, row, col);
         const int before = pc.j * (f.sp.seg / f.sp.sub), s0 = lin_first_slot(a, pc.s, pc.t0, f.sp.sub);
         for (int i = 0; i < before; ++i)
             fold_tile(S, f.sp.U + tile_at(s0 + i, a.H, h, tiles, tile), f.sp.dec[(size_t)(s0 + i) * a.H + h], row, half);
-        auto publish = [&]() {                // the bf16 copy that Q S reads
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t z[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] = pack_bf16x2(S[j * 8 + 2 * i], S[j * 8 + 2 * i + 1]);
-                *reinterpret_cast<uint4 *>(sm + L_::S + swz(row, (half * 4 + j) * 16)) = make_uint4(z[0], z[1], z[2], z[3]);
-            }
-            fence_async_smem();
-            warp_arrive(s_full);
-        };
-        if (n > 0) publish();
+        bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(tok0 + row) * a.H + h) * a.dv + col;
         bool ok = true;
-        for (int c = 0; c < n; ++c) {
-            const int st = c & 1, L = min(C, len - c * C);
-            ok = w.wait(dec_full + st, (c >> 1) & 1) && w.wait(full + st, (c >> 1) & 1);
+        for (int c = 0; c <= n; ++c) {
+            // the bf16 copy that chunk c's Q S reads, once the Q S before has
+            if (c > 0) ok = w.wait(q_free + ((c - 1) & 1), ((c - 1) >> 1) & 1);
             if (!ok) break;
-            const float2 whole = meta[st].whole;
-            if (vrow < L) {
-                weigh_row(sm + L_::V + st * ATOM, sm + L_::VP, vrow, vhalf, decay_until(dec[st], meta[st], vrow));
-            } else {                          // rows behind the sequence's end: zeros in every operand that is summed over rows
+            if (c < n) {
 #pragma unroll
-                for (int k = 0; k < 3; ++k) zero_row(sm + L_::VP + k * ATOM, vrow, vhalf * 4, 4);
-                zero_row(sm + L_::V + st * ATOM, vrow, vhalf * 4, 4);
-                zero_row(sm + L_::K + (st * 2 + vhalf) * ATOM, vrow, 0, 8);
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t z[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[i] = round_bf16x2(S[j * 4 + i]);
+                    *reinterpret_cast<uint4 *>(sm + L_::S + swz(row, (half * 4 + j) * 16)) = make_uint4(z[0], z[1], z[2], z[3]);
+                }
+                fence_async_smem();
+                warp_arrive(s_full);
             }
-            fence_async_smem();
-            warp_arrive(vp_full);
-            warp_arrive(dec_empty + st);
-            ok = w.wait(dl_full, c & 1);
-            if (!ok) break;
-            tc_fence_after();
-            add_delta(S, T_DL + lanes + half * 32, whole);
-            tc_fence_before();
-            if (c + 1 < n) publish();
+            if (c > 0) {                      // o of the chunk before
+                const int st = (c - 1) & 1, L = min(C, len - (c - 1) * C);
+                // factored: the row's 2^{G_t} is common to both parts (P holds the columns' 2^{-G_s})
+                const float fs = a.scale * decay_since(dec[st], row), fi = dec[st].factored ? fs : a.scale;
+                warp_arrive(dec_free + st);
+                const f32x2 fs2 = pk2(fs, fs), fi2 = pk2(fi, fi);
+                ok = w.wait(o_full, (c - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int p = 0; p < 32; p += 16) {
+                    float x[16], y[16];
+                    tmem_ld16x2(T_OI + lanes + half * 32 + p, T_OS + lanes + half * 32 + p, x, y);
+                    if (p == 16) {
+                        tc_fence_before();
+                        warp_arrive(o_free);
+                    }
+                    if (row < L && col < a.dv) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 8) {
+                            uint32_t z[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                z[i] = round_bf16x2(fma2(fi2, pk2(x[j + 2 * i], x[j + 2 * i + 1]), mul2(fs2, pk2(y[j + 2 * i], y[j + 2 * i + 1]))));
+                            *reinterpret_cast<uint4 *>(o + p + j) = make_uint4(z[0], z[1], z[2], z[3]);
+                        }
+                    }
+                }
+                o += (size_t)C * a.H * a.dv;
+            }
+            if (c < n) {
+                ok = w.wait(dec_full + (c & 1), (c >> 1) & 1) && w.wait(dl_full, c & 1);
+                if (!ok) break;
+                tc_fence_after();
+                add_delta(S, T_DL + lanes + half * 32, dec[c & 1].whole);
+                tc_fence_before();
+                warp_arrive(dl_free);
+            }
         }
         if (ok && a.S_out && (long long)(pc.j + 1) * f.sp.seg >= pc.len) store_caller(S, a.S_out + se, a.dk, a.dv, row, col);
-    } else if (warp == NW_A + NW_B) {
-        // ---------------------------------------------------------- TMA
+    } else if (warp == W_TMA) {
+        // ---------------------------------------------------------- TMA: Q, K and V are refilled as each is free
         if (lane == 0) {
-            const uint32_t bytes = (uint32_t)(2 * katoms + 1) * ATOM;
+            const Decay *decay = f.decay + (size_t)(lin_first_slot(a, pc.s, pc.t0, C) + pc.j * (f.sp.seg / C)) * a.H + h;
             for (int c = 0; c < n; ++c) {
                 const int st = c & 1, tok = tok0 + c * C;
-                if (c >= 2 && !w.wait(empty + st, ((c >> 1) - 1) & 1)) break;
+                const uint32_t before = ((c >> 1) - 1) & 1;
+                if (c >= 2 && !w.wait(q_free + st, before)) break;
                 if (*w.abort_flag) break;
-                mbar_expect_tx(full + st, bytes);
-                for (int k = 0; k < katoms; ++k) {
-                    load_tile(sm + L_::Q + (st * 2 + k) * ATOM, &f.tq, k * 64, h, tok, full + st);
-                    load_tile(sm + L_::K + (st * 2 + k) * ATOM, &f.tk, k * 64, h, tok, full + st);
-                }
-                load_tile(sm + L_::V + st * ATOM, &f.tv, tile * DVT, h, tok, full + st);
+                mbar_expect_tx(qk_full + st, (uint32_t)(2 * KATOMS) * ATOM);
+                for (int k = 0; k < KATOMS; ++k) load_tile(sm + L_::Q + (st * 2 + k) * ATOM, &f.tq, k * 64, h, tok, qk_full + st);
+                if (c >= 2 && !w.wait(k_free + st, before)) break;
+                for (int k = 0; k < KATOMS; ++k) load_tile(sm + L_::K + (st * 2 + k) * ATOM, &f.tk, k * 64, h, tok, qk_full + st);
+                if (c >= 2 && !w.wait(dec_free + st, before)) break;
+                mbar_expect_tx(dec_full + st, sizeof(Decay));
+                bulk_load(dec + st, decay + (size_t)c * a.H, sizeof(Decay), dec_full + st);
+                if (c >= 2 && !w.wait(v_free + st, before)) break;
+                mbar_expect_tx(v_full + st, ATOM);
+                load_tile(sm + L_::V + st * ATOM, &f.tv, tile * DVT, h, tok, v_full + st);
             }
         }
-    } else if (warp == NW_A + NW_B + 1) {
-        // ---------------------------------------------------------- MMA
-        if (lane == 0) {
-            constexpr uint32_t ID_QK = idesc_bf16(128, 128, false, false), ID_QS = idesc_bf16(128, 64, false, true);
-            auto qk = [&](int c) -> bool {
-                const int st = c & 1;
-                if (!w.wait(full + st, (c >> 1) & 1)) return false;
-                tc_fence_after();
-                for (int ks = 0; ks < 4 * katoms; ++ks)
-                    mma_bf16(T_SC + st * 128, kmajor(sb + L_::Q + st * 2 * ATOM, ks), kmajor(sb + L_::K + st * 2 * ATOM, ks), ID_QK, ks > 0);
-                mma_commit(sc_full + st);
-                return true;
-            };
-            bool ok = n == 0 || qk(0);
-            for (int c = 0; c < n && ok; ++c) {
-                const int st = c & 1;
-                ok = w.wait(s_full, c & 1) && (c == 0 || w.wait(o_free, (c - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
-                for (int ks = 0; ks < 4 * katoms; ++ks)
-                    mma_bf16(T_OS, kmajor(sb + L_::Q + st * 2 * ATOM, ks), mnmajor(sb + L_::S, ks), ID_QS, ks > 0);
-                ok = w.wait(vp_full, c & 1);
-                if (!ok) break;
-                tc_fence_after();
+    } else if (warp == W_MMA) {
+        // ---------------------------------------------------------- MMA (the warp waits, one lane issues)
+        const bool one = elect_one();
+        for (int c = 0; c < n; ++c) {
+            const int st = __shfl_sync(0xffffffffu, c & 1, 0);   // (uniform to the compiler: descriptors stay in uniform registers)
+            if (!w.wait(qk_full + st, (c >> 1) & 1)) break;
+            tc_fence_after();
+            if (one) {                        // (the scores before were read before P V of the chunk before)
+                mma_tiles<4 * KATOMS, false, false, 128>(T_SC, sb + L_::Q + st * 2 * ATOM, sb + L_::K + st * 2 * ATOM, false);
+                mma_commit(sc_full);
+            }
+            if (!w.wait(vp_full, c & 1) || (c > 0 && !w.wait(dl_free, (c - 1) & 1))) break;
+            tc_fence_after();
+            if (one) {
                 mma_delta(T_DL, sb + L_::K + st * 2 * ATOM, sb + L_::VP);
                 mma_commit(dl_full);
-                ok = w.wait(p_full + st, (c >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_bf16_ta(T_OI, T_SC + st * 128 + ks * 8, mnmajor(sb + L_::V + st * ATOM, ks), ID_QS, ks > 0);
-                mma_commit(o_full);
-                mma_commit(empty + st);
-                if (c + 1 < n) ok = qk(c + 1);
+                mma_commit(k_free + st);
             }
-        }
-    } else {
-        // ---------------------------------------------------------- decay
-        double x[4];
-        if (n > 0) decay_fetch(a, tok0, min(C, len), h, x);
-        for (int c = 0; c < n; ++c) {
-            const int st = c & 1;
-            if (c >= 2 && !w.wait(dec_empty + st, ((c >> 1) - 1) & 1)) break;
-            decay_write(x, dec + st, meta + st);
-            warp_arrive(dec_full + st);
-            if (c + 1 < n) decay_fetch(a, tok0 + (c + 1) * C, min(C, len - (c + 1) * C), h, x);
+            if (!w.wait(s_full, c & 1) || (c > 0 && !w.wait(o_free, (c - 1) & 1))) break;
+            tc_fence_after();
+            if (one) {
+                mma_tiles<4 * KATOMS, false, true, 64>(T_OS, sb + L_::Q + st * 2 * ATOM, sb + L_::S, false);
+                mma_commit(q_free + st);
+            }
+            if (!w.wait(p_full, c & 1)) break;
+            tc_fence_after();
+            if (one) {
+                const uint64_t dv = tile_mnmajor(sb + L_::V + st * ATOM);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_bf16_ta(T_OI, T_P + ks * 8, dv + step_mnmajor(ks), idesc_bf16(128, 64, false, true), ks > 0);
+                mma_commit(o_full);
+                mma_commit(v_free + st);
+            }
         }
     }
 
@@ -408,18 +440,23 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
         // a wait gave up: bounded waits for the copies and MMAs in flight, before their memory goes
         if (threadIdx.x == 0) {
             raise_error(a.err, ERR_TIMEOUT);
-            for (int i = 0; i < 2; ++i) drain(full + i, 0);
-            for (int i = 0; i < 2; ++i) drain(full + i, 1);
+            for (int i = 0; i < 2; ++i) {     // whichever phase is under way
+                for (uint32_t ph = 0; ph < 2; ++ph) {
+                    drain(qk_full + i, ph);
+                    drain(v_full + i, ph);
+                    drain(dec_full + i, ph);
+                }
+            }
         }
-        if (warp == NW_A + NW_B + 1 && lane == 0) {
-            mbar_init(o_free, 1);
+        if (warp == W_MMA && elect_one()) {
+            mbar_init(s_full, 1);
             mbar_fence_init();
-            mma_commit(o_free);
-            drain(o_free, 0);
+            mma_commit(s_full);
+            drain(s_full, 0);
         }
         __syncthreads();
     }
-    if (warp == NW_A + NW_B + 1) tmem_dealloc(tmem, 512);
+    if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
 // ================================================================= states
@@ -431,8 +468,8 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
 // state and the totals of the segments before, every chunk's value is stored.
 // The delta MMAs (896 cycles per chunk) hide the two epilogues: prep and state each have their own eight
 // warps and a second buffer of weighted rows and of TMEM columns.
-template <bool REV, bool TOTALS>
-__global__ void __launch_bounds__(NT_F, 1) linear_state_kernel(const __grid_constant__ StateArgs f)
+template <bool REV, bool TOTALS, int KATOMS>
+__global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_constant__ StateArgs f)
 {
     using L_ = StateSmem;
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -441,6 +478,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_state_kernel(const __grid_cons
     const int tiles = (a.dv + DVT - 1) / DVT;
     const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % a.H, u = blockIdx.x / tiles / a.H;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int W_MMA = NW_W + NW_S, W_TMA = W_MMA + 1;
     LinPiece pc;
     if (!lin_piece(a, u, f.piece, pc)) return;
     const int per = f.sp.seg / f.sp.sub;
@@ -450,8 +488,8 @@ __global__ void __launch_bounds__(NT_F, 1) linear_state_kernel(const __grid_cons
     }
     const int tok0 = pc.t0 + pc.j * f.piece, len = min(f.piece, pc.len - pc.j * f.piece);
     const int n = (len + C - 1) / C;
-    const int katoms = a.dk > 64 ? 2 : 1;
     auto chunk = [&](int c) { return REV ? n - 1 - c : c; };
+    const int c0 = lin_first_slot(a, pc.s, pc.t0, C) + pc.j * (f.piece / C);   // the piece's first chunk's slot
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L_::BAR);
     uint64_t *full = bar, *empty = bar + 2, *vp_full = bar + 4, *dl_full = bar + 6, *dl_free = bar + 8, *dec_full = bar + 10,
@@ -460,37 +498,36 @@ __global__ void __launch_bounds__(NT_F, 1) linear_state_kernel(const __grid_cons
     int *abort_flag = reinterpret_cast<int *>(sm + L_::CTL + 4);
     const Waits w{abort_flag};
     Decay *dec = reinterpret_cast<Decay *>(sm + L_::DEC);
-    DecayMeta *meta = reinterpret_cast<DecayMeta *>(sm + L_::META);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(full + i, 1);
             mbar_init(empty + i, 1);
-            mbar_init(vp_full + i, NW_A);
+            mbar_init(vp_full + i, NW_W);
             mbar_init(dl_full + i, 1);
-            mbar_init(dl_free + i, NW_B);
+            mbar_init(dl_free + i, NW_S);
             mbar_init(dec_full + i, 1);
-            mbar_init(dec_empty + i, NW_A + NW_B);
+            mbar_init(dec_empty + i, NW_W + NW_S);
         }
         mbar_fence_init();
         *abort_flag = (sb & 1023u) ? 1 : 0;
         tma_prefetch_desc(&f.tx);
         tma_prefetch_desc(&f.ty);
     }
-    if (katoms == 1) {
-        for (int i = threadIdx.x; i < 2 * (ATOM / 16); i += NT_F)
+    if (KATOMS == 1) {
+        for (int i = threadIdx.x; i < 2 * (ATOM / 16); i += NT_S)
             *reinterpret_cast<uint4 *>(sm + L_::X + (i / (ATOM / 16)) * 2 * ATOM + ATOM + (i % (ATOM / 16)) * 16) = make_uint4(0, 0, 0, 0);
         fence_async_smem();
     }
-    if (warp == NW_A + NW_B + 1) tmem_alloc(tmem_slot, 256);
+    if (warp == W_MMA) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t lanes = ((uint32_t)(warp & 3) * 32u) << 16;
     const int row = (warp & 3) * 32 + lane;
 
-    if (warp < NW_A) {
+    if (warp < NW_W) {
         // ---------------------------------------------------------- weighted rows
         const int vrow = threadIdx.x & 127, vhalf = threadIdx.x >> 7;
         for (int c = 0; c < n; ++c) {
@@ -500,7 +537,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_state_kernel(const __grid_cons
             uint8_t *vp = sm + L_::VP + st * 3 * ATOM;
             if (vrow < L) {
                 weigh_row(sm + L_::Y + st * ATOM, vp, vrow, vhalf,
-                          REV ? a.scale * decay_since(dec[st], meta[st].factored, vrow) : decay_until(dec[st], meta[st], vrow));
+                          REV ? a.scale * decay_since(dec[st], vrow) : decay_until(dec[st], vrow));
             } else {
 #pragma unroll
                 for (int k = 0; k < 3; ++k) zero_row(vp + k * ATOM, vrow, vhalf * 4, 4);
@@ -510,12 +547,12 @@ __global__ void __launch_bounds__(NT_F, 1) linear_state_kernel(const __grid_cons
             warp_arrive(vp_full + st);
             warp_arrive(dec_empty + st);
         }
-    } else if (warp < NW_A + NW_B) {
+    } else if (warp < W_MMA) {
         // ---------------------------------------------------------- the state
-        const int half = (warp - NW_A) >> 2;
+        const int half = (warp - NW_W) >> 2;
         const int col = tile * DVT + half * 32;
         const size_t se = ((size_t)pc.s * a.H + h) * a.dk * a.dv;
-        float S[32];
+        f32x2 S[16];
         load_caller(S, !TOTALS && f.first ? f.first + se : nullptr, a.dk, a.dv, row, col);
         if (!TOTALS) {
             const int s0 = lin_first_slot(a, pc.s, pc.t0, f.sp.sub);
@@ -525,68 +562,57 @@ __global__ void __launch_bounds__(NT_F, 1) linear_state_kernel(const __grid_cons
                 fold_tile(S, f.sp.U + tile_at(slot, a.H, h, tiles, tile), f.sp.dec[slot * a.H + h], row, half);
             }
         }
-        const int c0 = lin_first_slot(a, pc.s, pc.t0, C) + pc.j * (f.piece / C);
-        double log_whole = 0.0;
-        bool ok = true;
+        Log2 total = {0.f, 0.f};
+        bool ok = true, bad = false;
         for (int c = 0; c < n; ++c) {
             const int st = c & 1;
             if (!TOTALS) store_tile(S, f.tiles + tile_at(c0 + chunk(c), a.H, h, tiles, tile), row, half);
             ok = w.wait(dec_full + st, (c >> 1) & 1);
             if (!ok) break;
-            const float2 whole = meta[st].whole;
+            const float2 whole = dec[st].whole;
+            total = total + dec[st].total;
+            bad = bad || whole.x != whole.x;
             warp_arrive(dec_empty + st);
-            if (TOTALS && warp == NW_A) {     // the piece's decay: the product of the chunks', in fp64
-                const double x = (double)whole.x + (double)whole.y;
-                log_whole = c == 0 ? x : log_whole * x;
-            }
             ok = w.wait(dl_full + st, (c >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            add_delta(S, tmem + st * 128 + lanes + half * 32, whole);
+            add_delta(S, tmem + st * 192 + lanes + half * 32, whole);
             tc_fence_before();
             warp_arrive(dl_free + st);
         }
         if (ok && TOTALS) {
             store_tile(S, f.tiles + tile_at(u, a.H, h, tiles, tile), row, half);
-            if (warp == NW_A && lane == 0 && tile == 0) {
-                const float hi = (float)log_whole;
-                f.dec[(size_t)u * a.H + h] = make_float2(hi, (float)(log_whole - (double)hi));
-            }
+            if (warp == NW_W && lane == 0 && tile == 0)
+                f.dec[(size_t)u * a.H + h] = bad ? make_float2(__int_as_float(0x7fc00000), 0.f) : lin_chunk_decay(total);
         } else if (ok && f.last && (REV ? pc.j == 0 : (long long)(pc.j + 1) * f.piece >= pc.len)) {
             store_caller(S, f.last + se, a.dk, a.dv, row, col);
         }
-    } else if (warp == NW_A + NW_B) {
+    } else if (warp == W_TMA) {
         if (lane == 0) {
             for (int c = 0; c < n; ++c) {
                 const int st = c & 1, tok = tok0 + chunk(c) * C;
                 if (c >= 2 && !w.wait(empty + st, ((c >> 1) - 1) & 1)) break;
                 if (*w.abort_flag) break;
-                mbar_expect_tx(full + st, (uint32_t)(katoms + 1) * ATOM);
-                for (int k = 0; k < katoms; ++k) load_tile(sm + L_::X + (st * 2 + k) * ATOM, &f.tx, k * 64, h, tok, full + st);
+                mbar_expect_tx(full + st, (uint32_t)(KATOMS + 1) * ATOM);
+                if (c >= 2 && !w.wait(dec_empty + st, ((c >> 1) - 1) & 1)) break;
+                mbar_expect_tx(dec_full + st, sizeof(Decay));
+                bulk_load(dec + st, f.decay + (size_t)(c0 + chunk(c)) * a.H + h, sizeof(Decay), dec_full + st);
+                for (int k = 0; k < KATOMS; ++k) load_tile(sm + L_::X + (st * 2 + k) * ATOM, &f.tx, k * 64, h, tok, full + st);
                 load_tile(sm + L_::Y + st * ATOM, &f.ty, tile * DVT, h, tok, full + st);
             }
         }
-    } else if (warp == NW_A + NW_B + 1) {
-        if (lane == 0) {
-            for (int c = 0; c < n; ++c) {
-                const int st = c & 1;
-                if (!w.wait(full + st, (c >> 1) & 1) || !w.wait(vp_full + st, (c >> 1) & 1)) break;
-                if (c >= 2 && !w.wait(dl_free + st, ((c >> 1) - 1) & 1)) break;
-                tc_fence_after();
-                mma_delta(tmem + st * 128, sb + L_::X + st * 2 * ATOM, sb + L_::VP + st * 3 * ATOM);
+    } else if (warp == W_MMA) {
+        const bool one = elect_one();
+        for (int c = 0; c < n; ++c) {
+            const int st = __shfl_sync(0xffffffffu, c & 1, 0);
+            if (!w.wait(full + st, (c >> 1) & 1) || !w.wait(vp_full + st, (c >> 1) & 1)) break;
+            if (c >= 2 && !w.wait(dl_free + st, ((c >> 1) - 1) & 1)) break;
+            tc_fence_after();
+            if (one) {
+                mma_delta(tmem + st * 192, sb + L_::X + st * 2 * ATOM, sb + L_::VP + st * 3 * ATOM);
                 mma_commit(dl_full + st);
                 mma_commit(empty + st);
             }
-        }
-    } else {
-        double x[4];
-        if (n > 0) decay_fetch(a, tok0 + chunk(0) * C, min(C, len - chunk(0) * C), h, x);
-        for (int c = 0; c < n; ++c) {
-            const int st = c & 1;
-            if (c >= 2 && !w.wait(dec_empty + st, ((c >> 1) - 1) & 1)) break;
-            decay_write(x, dec + st, meta + st);
-            warp_arrive(dec_full + st);
-            if (c + 1 < n) decay_fetch(a, tok0 + chunk(c + 1) * C, min(C, len - chunk(c + 1) * C), h, x);
         }
     }
 
@@ -595,10 +621,14 @@ __global__ void __launch_bounds__(NT_F, 1) linear_state_kernel(const __grid_cons
     if (*abort_flag) {
         if (threadIdx.x == 0) {
             raise_error(a.err, ERR_TIMEOUT);
-            for (int i = 0; i < 2; ++i) drain(full + i, 0);
-            for (int i = 0; i < 2; ++i) drain(full + i, 1);
+            for (int i = 0; i < 2; ++i) {
+                for (uint32_t ph = 0; ph < 2; ++ph) {
+                    drain(full + i, ph);
+                    drain(dec_full + i, ph);
+                }
+            }
         }
-        if (warp == NW_A + NW_B + 1 && lane == 0) {
+        if (warp == W_MMA && elect_one()) {
             mbar_init(dl_free, 1);
             mbar_fence_init();
             mma_commit(dl_free);
@@ -606,7 +636,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_state_kernel(const __grid_cons
         }
         __syncthreads();
     }
-    if (warp == NW_A + NW_B + 1) tmem_dealloc(tmem, 256);
+    if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
 // ================================================================= host side
@@ -643,18 +673,25 @@ size_t totals_bytes(const LinArgs &a, int sub) {
     return round256((size_t)slots(a, sub) * a.H * tiles_of(a) * TILE_FLOATS * 4) + round256((size_t)slots(a, sub) * a.H * 8);
 }
 
+size_t decay_bytes(const LinArgs &a) { return round256((size_t)slots(a, C) * a.H * sizeof(Decay)); }
+cudaError_t decays(const LinArgs &a, void *ws, cudaStream_t st) {
+    const long long n = slots(a, C) * a.H;
+    linear_decay_kernel<<<(unsigned)((n + 7) / 8), 256, 0, st>>>(a, static_cast<Decay *>(ws), n);
+    return cudaGetLastError();
+}
+
 template <typename K>
-cudaError_t setup(K kern, size_t smem) {
+cudaError_t setup(K kern, size_t smem, int threads) {
     KernelSetup ks;
-    return kernel_setup(reinterpret_cast<const void *>(kern), smem, NT_F, false, &ks);
+    return kernel_setup(reinterpret_cast<const void *>(kern), smem, threads, false, &ks);
 }
 
 template <bool REV, bool TOTALS>
 cudaError_t states(const StateArgs &f, cudaStream_t st) {
-    auto kern = linear_state_kernel<REV, TOTALS>;
-    const cudaError_t e = setup(kern, StateSmem::TOTAL);
+    auto kern = f.a.dk > 64 ? linear_state_kernel<REV, TOTALS, 2> : linear_state_kernel<REV, TOTALS, 1>;
+    const cudaError_t e = setup(kern, StateSmem::TOTAL, NT_S);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(slots(f.a, f.piece) * f.a.H * tiles_of(f.a)), NT_F, StateSmem::TOTAL, st>>>(f);
+    kern<<<(unsigned)(slots(f.a, f.piece) * f.a.H * tiles_of(f.a)), NT_S, StateSmem::TOTAL, st>>>(f);
     return cudaGetLastError();
 }
 
@@ -683,7 +720,7 @@ cudaError_t totals(StateArgs f, uint8_t *ws, Split *sp, cudaStream_t st) {
 size_t linear_tc_workspace_bytes(const LinArgs &a) {
     int seg, sub;
     split_of(a, &seg, &sub);
-    return is_split(a, seg) ? totals_bytes(a, sub) : 0;
+    return decay_bytes(a) + (is_split(a, seg) ? totals_bytes(a, sub) : 0);
 }
 
 cudaError_t launch_linear_tc(const LinArgs &a, void *workspace, cudaStream_t st) {
@@ -696,10 +733,13 @@ cudaError_t launch_linear_tc(const LinArgs &a, void *workspace, cudaStream_t st)
     s.a = a;
     s.tx = f.tk;
     s.ty = f.tv;
-    cudaError_t e = totals<false>(s, static_cast<uint8_t *>(workspace), &f.sp, st);
-    if (e == cudaSuccess) e = setup(linear_forward_kernel, FwdSmem::TOTAL);
+    s.decay = f.decay = static_cast<const Decay *>(workspace);
+    cudaError_t e = decays(a, workspace, st);
+    if (e == cudaSuccess) e = totals<false>(s, static_cast<uint8_t *>(workspace) + decay_bytes(a), &f.sp, st);
+    auto kern = a.dk > 64 ? linear_forward_kernel<2> : linear_forward_kernel<1>;
+    if (e == cudaSuccess) e = setup(kern, FwdSmem::TOTAL, NT_F);
     if (e != cudaSuccess) return e;
-    linear_forward_kernel<<<(unsigned)(slots(a, f.sp.seg) * a.H * tiles_of(a)), NT_F, FwdSmem::TOTAL, st>>>(f);
+    kern<<<(unsigned)(slots(a, f.sp.seg) * a.H * tiles_of(a)), NT_F, FwdSmem::TOTAL, st>>>(f);
     return cudaGetLastError();
 }
 

@@ -19,19 +19,23 @@ constexpr int ATOM = C * 128;      // bytes of a [128 rows][64 bf16] swizzled ti
 // ------------------------------------------------------------------ waits
 // Every wait gives up after ~0.5 s of SM clocks, or as soon as another wait of the CTA has; the
 // kernels then stop issuing work and drain what is in flight.
+// (The slow path is a call, the hot loops are kept rolled and the sizes template arguments: the roles of a
+// kernel run side by side, and together they have to stay in the instruction cache.)
+__device__ __noinline__ bool wait_slowly(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait_for(bar, parity, 1000000u)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > 1000000000ll) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
 struct Waits {
     volatile int *abort_flag;
     __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
-        if (mbar_try_wait(bar, parity)) return true;
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar, parity)) {
-            if (*abort_flag) return false;
-            if (clock64() - t0 > 1000000000ll) {
-                *abort_flag = 1;
-                return false;
-            }
-        }
-        return true;
+        return mbar_try_wait_for(bar, parity, 1000000u) || wait_slowly(bar, parity, abort_flag);
     }
 };
 // all lanes' writes before this are behind the arrival of the warp's one lane
@@ -41,81 +45,60 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
 }
 
 // ------------------------------------------------------------------ decay of a chunk
-// With G the chunk's inclusive log2 decays (fp64): where |G| <= 60 throughout, e^{-G_s} is stored and
-// every factor is a product of stored ones (no exponential per pair); in a chunk that decays further
-// (or a reset) G itself is stored in two floats and the factors are formed pair by pair, so that none
-// exceeds one.
-struct Decay {
+// A small launch ahead (linear_decay_kernel) forms one record per (chunk, head), which every kernel that walks
+// the chunk fetches with a bulk copy: the factors' arithmetic is long for one warp between two chunks, and
+// would be repeated by every tile of d_v and by the backward's three walks.
+// With G the chunk's inclusive log2 decays: where |G| <= 60 throughout, 2^{-G_s} is stored and every factor is
+// a product of stored ones (no exponential per pair); in a chunk that decays further (or a reset) G itself is
+// stored in two floats and the factors are formed pair by pair, so that none exceeds one.  Behind the
+// sequence's end the decay is 1.  A NaN among the log decays makes all of the chunk's factors NaN.
+struct __align__(16) Decay {
     float b[C];                    // factored: 2^{-G_s};  pairwise: high part of G_s
     float lo[C];                   // pairwise: low part
-};
-struct DecayMeta {
     float2 whole;                  // the whole chunk's decay, in two floats
+    Log2 total;                    // its log2
     int factored;
-    int pad;
+    int pad[3];
 };
-__device__ __forceinline__ float decay_since(const Decay &d, bool factored, int t) {   // 2^{G_t}
-    return factored ? 1.f / d.b[t] : exp2f(d.b[t] + d.lo[t]);
+static_assert(sizeof(Decay) % 16 == 0, "bulk copies");
+__device__ __forceinline__ float decay_since(const Decay &d, int t) {   // 2^{G_t}
+    return d.factored ? 1.f / d.b[t] : exp2f(d.b[t] + d.lo[t]);
 }
-__device__ __forceinline__ float decay_until(const Decay &d, const DecayMeta &m, int s) {   // 2^{G_C - G_s}
-    return m.factored ? m.whole.x * d.b[s] : exp2f((d.b[C - 1] - d.b[s]) + (d.lo[C - 1] - d.lo[s]));
+__device__ __forceinline__ float decay_until(const Decay &d, int s) {   // 2^{G_C - G_s}
+    return d.factored ? d.whole.x * d.b[s] : exp2f((d.b[C - 1] - d.b[s]) + (d.lo[C - 1] - d.lo[s]));
 }
 __device__ __forceinline__ float decay_pair(const Decay &d, int t, int s) {   // 2^{G_t - G_s}, pairwise chunks
     return exp2f((d.b[t] - d.b[s]) + (d.lo[t] - d.lo[s]));
 }
 
-// one warp: the factors of the chunk whose tokens' log2 decays x (four per lane) were fetched before
-__device__ __forceinline__ void decay_fetch(const LinArgs &a, int tok, int L, int h, double (&x)[4]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = lane * 4 + i < L ? lin_log2_decay(a, tok + lane * 4 + i, h) : 0.0;
-}
-__device__ __forceinline__ void decay_write(const double (&x)[4], Decay *d, DecayMeta *m) {
-    const int lane = threadIdx.x & 31;
-    double G[4];
-    G[0] = x[0];
-#pragma unroll
-    for (int i = 1; i < 4; ++i) G[i] = G[i - 1] + x[i];
-    double s = G[3];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += y;
-    }
-    const double before = s - G[3];
-    bool in = true;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        G[i] += before;
-        in = in && G[i] >= -60.0 && G[i] <= 60.0;
-    }
-    const bool factored = __all_sync(0xffffffffu, in);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float hi = (float)G[i];
-        d->b[lane * 4 + i] = factored ? lin_exp2(-G[i]) : hi;
-        if (!factored) d->lo[lane * 4 + i] = (float)(G[i] - (double)hi);
-    }
-    if (lane == 31) {
-        m->whole = lin_chunk_decay(s);
-        m->factored = factored;
-    }
-}
-
 // ------------------------------------------------------------------ three bf16 terms of an fp32 value
-// x = t0 + t1 + t2 up to 2^-24 |x|: the products that fp32 states are summed from keep fp32's accuracy
-// through bf16 operands (two terms alone would leave 2^-17)
-__device__ __forceinline__ void split3(float x, float y, uint32_t (&t)[3]) {
-    t[0] = pack_bf16x2(x, y);
-    x -= bf16_lo(t[0]);
-    y -= bf16_hi(t[0]);
-    t[1] = pack_bf16x2(x, y);
-    t[2] = pack_bf16x2(x - bf16_lo(t[1]), y - bf16_hi(t[1]));
+// x = t0 + t1 + t2 exactly (barring underflow): each term takes the leading 8 of the 24 bits that are left, by
+// truncation.  So the products that fp32 states are summed from keep fp32's accuracy through bf16 operands
+// (two terms would leave 2^-16).  No conversion instruction: cvt.rn.bf16x2 runs at about 8 lanes per clock and
+// SM, which bounded the whole kernel when every packing used it (XU pipe 89% busy).
+__device__ __forceinline__ f32x2 unpack2(uint32_t u) { return pk2(bf16_lo(u), bf16_hi(u)); }
+__device__ __forceinline__ uint32_t upper_halves(f32x2 x) {   // two bf16 by truncation
+    return __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
+}
+__device__ __forceinline__ f32x2 trunc2(f32x2 x) { return x & 0xffff0000ffff0000ull; }
+__device__ __forceinline__ void split3(f32x2 x, uint32_t (&t)[3]) {
+    t[0] = upper_halves(x);
+    x = sub2(x, trunc2(x));
+    t[1] = upper_halves(x);
+    x = sub2(x, trunc2(x));
+    t[2] = upper_halves(x);
+}
+// two fp32 rounded to nearest bf16 on the FMA pipe: with c = (2^16 + 1) x, c - (c - x) has the leading 8
+// bits (Veltkamp's splitting; beyond 2^111 the result is not a number, as for an infinity).  c is a rounded fma:
+// a packed product may be contracted with the subtraction, which would undo the rounding it is there for.
+__device__ __forceinline__ uint32_t round_bf16x2(f32x2 x) {
+    const f32x2 c = fma2(x, pk2(65536.f, 65536.f), x);
+    return upper_halves(sub2(c, sub2(c, x)));
 }
 
 // half a row of a [128][64] bf16 tile, weighted, as three terms in three tiles (thread = row x half)
 __device__ __forceinline__ void weigh_row(const uint8_t *src, uint8_t *dst, int row, int half, float w) {
-#pragma unroll
+#pragma unroll 2
     for (int j = 0; j < 4; ++j) {
         const uint32_t off = swz(row, (half * 4 + j) * 16);
         const uint4 u = *reinterpret_cast<const uint4 *>(src + off);
@@ -124,7 +107,7 @@ __device__ __forceinline__ void weigh_row(const uint8_t *src, uint8_t *dst, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t t[3];
-            split3(bf16_lo(x[i]) * w, bf16_hi(x[i]) * w, t);
+            split3(mul2(unpack2(x[i]), pk2(w, w)), t);
             o[0][i] = t[0]; o[1][i] = t[1]; o[2][i] = t[2];
         }
 #pragma unroll
@@ -137,22 +120,31 @@ __device__ __forceinline__ void zero_row(uint8_t *dst, int row, int first, int n
 }
 
 // ------------------------------------------------------------------ MMAs (one thread)
-// D[128, n] (+)= A B over 16-element K steps; shared-memory operands in 128-byte swizzled tiles
-__device__ __forceinline__ uint64_t kmajor(uint32_t tile, int step) {   // K along the rows' 128 bytes, 64 elements per tile
-    return sdesc(tile + (uint32_t)(step >> 2) * ATOM + (uint32_t)(step & 3) * 32u, 16, 1024);
-}
-__device__ __forceinline__ uint64_t mnmajor(uint32_t tile, int step) {  // K along the tile's rows, MN in blocks of 64
-    return sdesc(tile + (uint32_t)step * 2048u, ATOM, 1024);
-}
+// D[128, n] (+)= A B over 16-element K steps; shared-memory operands in 128-byte swizzled tiles.  The
+// steps' descriptors differ from the tile's by a constant (the address field holds address / 16), so the
+// issuing thread spends one addition per operand and step.
+__device__ __forceinline__ uint64_t tile_kmajor(uint32_t tile) { return sdesc(tile, 16, 1024); }    // K along the rows' 128 bytes, 64 elements per tile
+__device__ __forceinline__ uint64_t tile_mnmajor(uint32_t tile) { return sdesc(tile, ATOM, 1024); } // K along the tile's rows, MN in blocks of 64
+__host__ __device__ constexpr uint32_t step_kmajor(int ks) { return ((ks >> 2) * ATOM + (ks & 3) * 32) >> 4; }
+__host__ __device__ constexpr uint32_t step_mnmajor(int ks) { return ks * 2048 >> 4; }
 
-// delta[dk, dv tile] = X^T (Y0 + Y1 + Y2): columns 0..63 take the first term, 64..127 the other two
-__device__ __forceinline__ void mma_delta(uint32_t d, uint32_t x, uint32_t y) {
-    constexpr uint32_t ID2 = idesc_bf16(128, 128, true, true), ID1 = idesc_bf16(128, 64, true, true);
+// D (+)= A B over STEPS K steps (a multiple of 4), both operands in shared memory
+template <int STEPS, bool A_MN, bool B_MN, int N>
+__device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a, uint32_t b, bool acc) {
+    constexpr uint32_t ID = idesc_bf16(128, N, A_MN, B_MN);
+    uint64_t da = A_MN ? tile_mnmajor(a) : tile_kmajor(a), db = B_MN ? tile_mnmajor(b) : tile_kmajor(b);
+#pragma unroll 1
+    for (int k4 = 0; k4 < STEPS / 4; ++k4) {
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) mma_bf16(d, mnmajor(x, ks), mnmajor(y, ks), ID2, ks > 0);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) mma_bf16(d + 64, mnmajor(x, ks), mnmajor(y + 2 * ATOM, ks), ID1, 1);
+        for (int ks = 0; ks < 4; ++ks)
+            mma_bf16(d, da + (A_MN ? step_mnmajor(ks) : step_kmajor(ks)), db + (B_MN ? step_mnmajor(ks) : step_kmajor(ks)), ID, acc || ks > 0);
+        da += A_MN ? step_mnmajor(4) : step_kmajor(4);
+        db += B_MN ? step_mnmajor(4) : step_kmajor(4);
+        acc = true;
+    }
 }
+// delta[dk, dv tile] = X^T [Y0 Y1 Y2]: 64 columns for each term, so that X is read from shared memory once
+__device__ __forceinline__ void mma_delta(uint32_t d, uint32_t x, uint32_t y) { mma_tiles<8, true, true, 192>(d, x, y, false); }
 
 // ------------------------------------------------------------------ states in the workspace
 // One tile of 64 columns of a [d_k, d_v] fp32 state: [16 column quads][128 rows][4].  A warp whose lanes
