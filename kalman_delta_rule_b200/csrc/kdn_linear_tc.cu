@@ -128,6 +128,11 @@ __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, in
     tma_load_3d(dst + ATOM / 2, m, c0, h, tok + 64, bar);
 }
 
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap *m, int c0, int h, int tok) {
+    tma_prefetch_3d(m, c0, h, tok);
+    tma_prefetch_3d(m, c0, h, tok + 64);
+}
+
 // after a wait gave up: one more bounded wait for a barrier that copies or MMAs in flight still arrive on
 __device__ __noinline__ void drain(uint64_t *bar, uint32_t parity) { mbar_wait(bar, parity, 100000000ll); }
 
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
             mbar_init(v_full + i, 1);
             mbar_init(q_free + i, 1);
             mbar_init(k_free + i, 1);
-            mbar_init(v_free + i, 1);
+            mbar_init(v_free + i, NW_S);
             mbar_init(dec_full + i, 1);
             mbar_init(dec_free + i, NW_W + NW_S);
         }
@@ -319,7 +324,10 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
         const int before = pc.j * (f.sp.seg / f.sp.sub), s0 = lin_first_slot(a, pc.s, pc.t0, f.sp.sub);
         for (int i = 0; i < before; ++i)
             fold_tile(S, f.sp.U + tile_at(s0 + i, a.H, h, tiles, tile), f.sp.dec[(size_t)(s0 + i) * a.H + h], row, half);
-        bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(tok0 + row) * a.H + h) * a.dv + col;
+        // the outputs go through the chunk's V tile, which its MMAs are done with: a warp's 32 rows x 64 bytes there
+        // and back, so that four lanes share a row's 64 bytes in memory (a row per lane costs 4 times the LSU cycles)
+        bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(tok0 + (warp & 3) * 32 + (lane >> 2)) * a.H + h) * a.dv + col + (lane & 3) * 8;
+        float fs = 0.f, fi = 0.f;
         bool ok = true;
         for (int c = 0; c <= n; ++c) {
             // the bf16 copy that chunk c's Q S reads, once the Q S before has
@@ -338,9 +346,6 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
             }
             if (c > 0) {                      // o of the chunk before
                 const int st = (c - 1) & 1, L = min(C, len - (c - 1) * C);
-                // factored: the row's 2^{G_t} is common to both parts (P holds the columns' 2^{-G_s})
-                const float fs = a.scale * decay_since(dec[st], row), fi = dec[st].factored ? fs : a.scale;
-                warp_arrive(dec_free + st);
                 const f32x2 fs2 = pk2(fs, fs), fi2 = pk2(fi, fi);
                 ok = w.wait(o_full, (c - 1) & 1);
                 if (!ok) break;
@@ -353,17 +358,24 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
                         tc_fence_before();
                         warp_arrive(o_free);
                     }
-                    if (row < L && col < a.dv) {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 8) {
-                            uint32_t z[4];
+                    for (int j = 0; j < 16; j += 8) {
+                        uint32_t z[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                z[i] = round_bf16x2(fma2(fi2, pk2(x[j + 2 * i], x[j + 2 * i + 1]), mul2(fs2, pk2(y[j + 2 * i], y[j + 2 * i + 1]))));
-                            *reinterpret_cast<uint4 *>(o + p + j) = make_uint4(z[0], z[1], z[2], z[3]);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            z[i] = round_bf16x2(fma2(fi2, pk2(x[j + 2 * i], x[j + 2 * i + 1]), mul2(fs2, pk2(y[j + 2 * i], y[j + 2 * i + 1]))));
+                        *reinterpret_cast<uint4 *>(sm + L_::V + st * ATOM + swz(row, half * 64 + (p + j) * 2)) = make_uint4(z[0], z[1], z[2], z[3]);
                     }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int r = 0; r < 32; r += 8) {
+                    const int t = (warp & 3) * 32 + r + (lane >> 2);
+                    const uint4 z = *reinterpret_cast<const uint4 *>(sm + L_::V + st * ATOM + swz(t, half * 64 + (lane & 3) * 16));
+                    if (t < L && col < a.dv) *reinterpret_cast<uint4 *>(o + (size_t)r * a.H * a.dv) = z;
+                }
+                fence_async_smem();
+                warp_arrive(v_free + st);
                 o += (size_t)C * a.H * a.dv;
             }
             if (c < n) {
@@ -373,6 +385,10 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
                 add_delta(S, T_DL + lanes + half * 32, dec[c & 1].whole);
                 tc_fence_before();
                 warp_arrive(dl_free);
+                // factored: the row's 2^{G_t} is common to both parts of o (P holds the columns' 2^{-G_s})
+                fs = a.scale * decay_since(dec[c & 1], row);
+                fi = dec[c & 1].factored ? fs : a.scale;
+                warp_arrive(dec_free + (c & 1));
             }
         }
         if (ok && a.S_out && (long long)(pc.j + 1) * f.sp.seg >= pc.len) store_caller(S, a.S_out + se, a.dk, a.dv, row, col);
@@ -383,6 +399,15 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
             for (int c = 0; c < n; ++c) {
                 const int st = c & 1, tok = tok0 + c * C;
                 const uint32_t before = ((c >> 1) - 1) & 1;
+                // two stages are one chunk ahead, less than DRAM's latency: the chunk two further on is brought into L2
+                if (c + 2 < n) {
+#pragma unroll 1
+                    for (int k = 0; k < KATOMS; ++k) {
+                        prefetch_tile(&f.tq, k * 64, h, tok + 2 * C);
+                        prefetch_tile(&f.tk, k * 64, h, tok + 2 * C);
+                    }
+                    prefetch_tile(&f.tv, tile * DVT, h, tok + 2 * C);
+                }
                 if (c >= 2 && !w.wait(q_free + st, before)) break;
                 if (*w.abort_flag) break;
                 mbar_expect_tx(qk_full + st, (uint32_t)(2 * KATOMS) * ATOM);
@@ -429,7 +454,6 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
                 for (int ks = 0; ks < 8; ++ks)
                     mma_bf16_ta(T_OI, T_P + ks * 8, dv + step_mnmajor(ks), idesc_bf16(128, 64, false, true), ks > 0);
                 mma_commit(o_full);
-                mma_commit(v_free + st);
             }
         }
     }
