@@ -79,6 +79,10 @@ cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, bool bf16_in, void 
 // tensor-core path in chunks of 128 tokens (bf16 inputs)
 size_t linear_tc_workspace_bytes(const LinArgs &a);
 cudaError_t launch_linear_tc(const LinArgs &a, void *workspace, cudaStream_t st);
+size_t linear_tc_backward_workspace_bytes(const LinArgs &a);
+cudaError_t launch_linear_tc_backward(const LinBwdArgs &b, void *workspace, cudaStream_t st);
+// dg [H] of a per-head decay from the shares [slots, H] of chunks of `tokens` tokens, in a fixed order
+cudaError_t launch_linear_head_decay(const LinArgs &a, const float *share, float *dg, int tokens, cudaStream_t st);
 // n tokens of N sequences on a state updated in place
 cudaError_t launch_linear_decode(const LinArgs &a, bool bf16_in, cudaStream_t st);
 

@@ -52,6 +52,9 @@ bool on_tensor_cores(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
 size_t forward_bytes(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
     return on_tensor_cores(p, a) ? kdn::linear_tc_workspace_bytes(a) : kdn::linear_simt_workspace_bytes(a);
 }
+size_t backward_bytes(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
+    return on_tensor_cores(p, a) ? kdn::linear_tc_backward_workspace_bytes(a) : kdn::linear_simt_backward_workspace_bytes(a);
+}
 
 kdn_status_t check_norm(long long n, int G, int d, kdn_dtype_t dtype, float eps) {
     if (n < 0 || G <= 0 || d <= 0 || !(eps >= 0.f) || !isfinite(eps)) return KDN_ERR_INVALID_ARG;
@@ -114,7 +117,7 @@ kdn_status_t kdn_linear_backward_workspace_size(const kdn_linear_problem_t *p, s
     const kdn_status_t st = check_problem(p, &a);
     if (st != KDN_OK) return st;
     if (!bytes) return KDN_ERR_INVALID_ARG;
-    *bytes = kdn::linear_simt_backward_workspace_bytes(a);
+    *bytes = backward_bytes(p, a);
     return KDN_OK;
 }
 
@@ -135,12 +138,13 @@ kdn_status_t kdn_linear_backward(const kdn_linear_problem_t *p, const void *q, c
     if (a.ntok > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv || (a.decay != KDN_DECAY_NONE && !g)))
         return KDN_ERR_INVALID_ARG;
     if (dS0 && dS0 == dS_T) return KDN_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < kdn::linear_simt_backward_workspace_bytes(a) ||
+    if (!workspace || workspace_bytes < backward_bytes(p, a) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return KDN_ERR_WORKSPACE;
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0;
     a.err = kdn::error_word();
     b.d_o = d_o; b.dS_T = dS_T; b.dq = dq; b.dk = dk; b.dv = dv; b.dg = dg; b.dS0 = dS0;
+    if (on_tensor_cores(p, a)) return cuda_status(kdn::launch_linear_tc_backward(b, workspace, cs));
     return cuda_status(kdn::launch_linear_simt_backward(b, p->in_dtype == KDN_DTYPE_BF16, workspace, cs));
 }
 

@@ -1,0 +1,450 @@
+// Backward of linear attention with a decay for each head on the tensor cores (tcgen05, bf16 inputs).
+// The states S at the chunks' starts and the state gradients R at their ends come from two walks over the
+// sequence (kdn_linear_tc.cu); everything else is parallel over (chunk, head), one CTA each.  With
+// a_t = scale e^{G_t}, w_t = e^{G_C - G_t}, P = scale Q K^T o D, dP = dO V^T, dA = scale dP o D, Z = P o dP:
+//     dQ = dA K + a (dO S^T),   dK = dA^T Q + w (V R^T),   dV = P^T dO + w (K R)
+//     dg_t = sum_{s >= t} (rows Z - columns Z)_s + sum_{s >= t} q_s.(a dO S^T)_s + sum_{s < t} k_s.(w V R^T)_s + e^{G_C} <S, R>
+// (no term is divided by a decay; none of the four sums cancels against another).
+//
+// TMEM holds four accumulators of 128 columns: the scores, dP, dO S^T and V R^T.  The last two are scaled
+// by their rows' decays in place, and dA K and dA^T Q are added to them; the first two are replaced by the
+// two parts of dV.  Rounding: P and dA, and R in K R, are bf16 (dq, dk and dv are); S and R enter the
+// products that dg is summed from as three bf16 terms, so dg keeps fp32's accuracy.
+// Per chunk and head at d = 128: 12 products of 128 x 128 x 128 (6100 cycles of MMA), 352 KB in and 96 KB out.
+#include "kdn_launch.h"
+#include "kdn_linear_tc.cuh"
+
+namespace kdn {
+
+using namespace lin;
+
+namespace {
+
+constexpr int NT = 512;
+
+struct Smem {
+    static constexpr int Q = 0, K = Q + 2 * ATOM, DO = K + 2 * ATOM, V = DO + 2 * ATOM, ST = V + 2 * ATOM, R1 = ST + 3 * ATOM,
+                         DEC = R1 + 2 * ATOM, SUM = DEC + (int)sizeof(Decay), CTL = SUM + (4 * 4 * C + 32) * 4, TOTAL = CTL + 32;
+    static constexpr int P = ST, DA = V;      // once the states' terms and V have been used
+};
+static_assert(Smem::TOTAL <= 227 * 1024, "shared memory");
+
+struct GradArgs {
+    LinBwdArgs b;
+    States s;
+    CUtensorMap tq, tk, tv, to;
+};
+
+// sums over the 32 lanes of 16 values each: lane l returns the sum of value l / 2
+__device__ __forceinline__ float sum16(float (&x)[16], int lane) {
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) {
+        const bool up = lane & (2 * w);       // lanes of the upper half keep the upper values
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float send = up ? x[i] : x[i + w], keep = up ? x[i + w] : x[i];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * w);
+        }
+    }
+    return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
+}
+
+}  // namespace
+
+template <int KATOMS>       // 64-channel tiles of q and k in use
+__global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_constant__ GradArgs f)
+{
+    using L_ = Smem;
+    constexpr int NK = 64 * KATOMS;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    const LinArgs &a = f.b.a;
+    const int u = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    LinPiece pc;
+    if (!lin_piece(a, u, C, pc) || pc.len == 0) return;
+    const int tok = pc.t0 + pc.j * C, L = min(C, pc.len - pc.j * C);
+    const int tiles = (a.dv + DVT - 1) / DVT, nt = min(tiles, 2);        // tiles of d_v, of a half that is resident
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp & 3, cg = warp >> 2;
+    const int row = q4 * 32 + lane;
+    const uint32_t lanes = ((uint32_t)q4 * 32u) << 16;
+
+    uint64_t *bar_tma = reinterpret_cast<uint64_t *>(sm + L_::CTL), *bar_mma = bar_tma + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_mma + 1);
+    int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+    const Waits w{abort_flag};
+    const Decay &d = *reinterpret_cast<const Decay *>(sm + L_::DEC);
+    float *zr = reinterpret_cast<float *>(sm + L_::SUM), *zc = zr + 4 * C, *xi = zc + 4 * C, *yi = xi + 4 * C, *sr_w = yi + 4 * C;
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar_tma, 1);
+        mbar_init(bar_mma, 1);
+        mbar_fence_init();
+        *abort_flag = (sb & 1023u) ? 1 : 0;
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const uint32_t T_SC = tmem, T_DP = tmem + 128, T_DQ = tmem + 256, T_DK = tmem + 384;
+    const bool one = warp == 0 && elect_one();
+    // every thread takes every wait and every barrier; after a wait that gave up the rest give up at once
+    uint32_t ph_tma = 0, ph_mma = 0;
+    auto wait_tma = [&]() { w.wait(bar_tma, ph_tma); ph_tma ^= 1; };
+    auto wait_mma = [&]() { w.wait(bar_mma, ph_mma); ph_mma ^= 1; tc_fence_after(); };
+    auto publish = [&]() {                    // this thread's shared-memory and TMEM work, before the next MMAs
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+    auto load_half = [&](int t0, bool first) {
+        if (threadIdx.x == 0) {
+            mbar_expect_tx(bar_tma, (uint32_t)((first ? 2 * KATOMS + nt : 0) + nt) * ATOM + (first ? (uint32_t)sizeof(Decay) : 0u));
+            if (first) {
+                bulk_load(sm + L_::DEC, f.s.decay + (size_t)u * a.H + h, sizeof(Decay), bar_tma);
+                for (int k = 0; k < KATOMS; ++k) {
+                    load_tile(sm + L_::Q + k * ATOM, &f.tq, k * 64, h, tok, bar_tma);
+                    load_tile(sm + L_::K + k * ATOM, &f.tk, k * 64, h, tok, bar_tma);
+                }
+                for (int t = 0; t < nt; ++t) load_tile(sm + L_::V + t * ATOM, &f.tv, (t0 + t) * DVT, h, tok, bar_tma);
+            }
+            for (int t = 0; t < nt; ++t) load_tile(sm + L_::DO + t * ATOM, &f.to, (t0 + t) * DVT, h, tok, bar_tma);
+        }
+    };
+    // 16 columns of a state tile's row in registers, and as terms in shared memory
+    auto fetch = [&](const float *base, int t, float4 (&x)[4]) {
+        const float *tile = base + tile_at(u, a.H, h, tiles, t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __ldg(reinterpret_cast<const float4 *>(tile + ((cg * 4 + j) * 128 + row) * 4));
+    };
+    auto terms = [&](const float4 (&x)[4], int p0, int p1, int p2) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t o[3][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 y = x[2 * j + (i >> 1)];
+                uint32_t t[3];
+                split3(i & 1 ? pk2(y.z, y.w) : pk2(y.x, y.y), t);
+                o[0][i] = t[0]; o[1][i] = t[1]; o[2][i] = t[2];
+            }
+            const uint32_t off = swz(row, (cg * 2 + j) * 16);
+            *reinterpret_cast<uint4 *>(sm + p0 + off) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+            *reinterpret_cast<uint4 *>(sm + p1 + off) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+            *reinterpret_cast<uint4 *>(sm + p2 + off) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
+        }
+    };
+    auto zero_tail = [&](int tile, int n) {   // rows behind the sequence's end
+        if (L < C && row >= L)
+            for (int t = 0; t < n; ++t) zero_row(sm + tile + t * ATOM, row, cg * 2, 2);
+    };
+
+    // ---- products with the states, half of d_v (two tiles) after half; the scores in the first one
+    float sr = 0.f;
+    float4 S[4], R[4];
+    for (int t0 = 0; t0 < tiles; t0 += 2) {
+        if (t0 == 0) {
+            load_half(0, true);
+            fetch(f.s.S, 0, S);
+        } else if (threadIdx.x == 0) {        // (the products that read the first half's tiles were waited for)
+            mbar_expect_tx(bar_tma, (uint32_t)(2 * nt) * ATOM);
+            for (int t = 0; t < nt; ++t) {
+                load_tile(sm + L_::V + t * ATOM, &f.tv, (t0 + t) * DVT, h, tok, bar_tma);
+                load_tile(sm + L_::DO + t * ATOM, &f.to, (t0 + t) * DVT, h, tok, bar_tma);
+            }
+        }
+        wait_tma();
+        if (t0 == 0) {
+            zero_tail(L_::Q, KATOMS);
+            zero_tail(L_::K, KATOMS);
+        }
+        zero_tail(L_::V, nt);
+        zero_tail(L_::DO, nt);
+        for (int t = 0; t < nt; ++t) {
+            terms(S, L_::ST, L_::ST + ATOM, L_::ST + 2 * ATOM);
+            fetch(f.s.R, t0 + t, R);
+            publish();
+            if (one) {
+                if (t == 0) {
+                    if (t0 == 0) mma_tiles<4 * KATOMS, false, false, 128>(T_SC, sb + L_::Q, sb + L_::K, false);
+                    for (int i = 0; i < nt; ++i) mma_tiles<4, false, false, 128>(T_DP, sb + L_::DO + i * ATOM, sb + L_::V + i * ATOM, t0 + i > 0);
+                }
+#pragma unroll 1
+                for (int p = 0; p < 3; ++p) mma_tiles<4, false, false, NK>(T_DQ, sb + L_::DO + t * ATOM, sb + L_::ST + p * ATOM, t0 + t + p > 0);
+                mma_commit(bar_mma);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sr += S[j].x * R[j].x + S[j].y * R[j].y + S[j].z * R[j].z + S[j].w * R[j].w;
+            if (t0 + t + 1 < tiles) fetch(f.s.S, t0 + t + 1, S);
+            wait_mma();
+            terms(R, L_::R1 + t * ATOM, L_::ST + ATOM, L_::ST + 2 * ATOM);
+            publish();
+            if (one) {
+                mma_tiles<4, false, false, NK>(T_DK, sb + L_::V + t * ATOM, sb + L_::R1 + t * ATOM, t0 + t > 0);
+#pragma unroll 1
+                for (int p = 1; p < 3; ++p) mma_tiles<4, false, false, NK>(T_DK, sb + L_::V + t * ATOM, sb + L_::ST + p * ATOM, true);
+                mma_commit(bar_mma);
+            }
+            wait_mma();
+        }
+    }
+
+    // ---- P and dA (bf16) to shared memory; the rows' and columns' sums of Z
+    const float since = decay_since(d, row), until = decay_until(d, row);
+    {
+        float z = 0.f;
+#pragma unroll 1
+        for (int p = 0; p < 32; p += 16) {
+            const int c0 = cg * 32 + p;
+            uint32_t pb[8] = {}, ab[8] = {};
+            if (cg <= q4) {
+                float x[16], y[16];
+                tmem_ld16x2(T_SC + lanes + c0, T_DP + lanes + c0, x, y);
+                const bool diagonal = cg == q4;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float g = a.scale * (d.factored ? since * d.b[c0 + j] : decay_pair(d, row, c0 + j));
+                    if (diagonal && c0 + j > row) g = 0.f;
+                    const float s = g == 0.f ? 0.f : x[j] * g, t = g == 0.f ? 0.f : y[j] * g;   // above the diagonal whatever the product holds
+                    x[j] = s;
+                    y[j] = t;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    pb[j] = round_bf16x2(pk2(x[2 * j], x[2 * j + 1]));
+                    ab[j] = round_bf16x2(pk2(y[2 * j], y[2 * j + 1]));
+                }
+                // Z = P dP: dP again, without the factor (a second read costs less than 16 registers)
+                float dp[16];
+                tmem_ld16(T_DP + lanes + c0, dp);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    x[j] = x[j] == 0.f ? 0.f : x[j] * dp[j];
+                    z += x[j];
+                }
+                const float s = sum16(x, lane);
+                if (!(lane & 1)) zc[q4 * C + c0 + (lane >> 1)] = s;
+            } else if (!(lane & 1)) {
+                zc[q4 * C + c0 + (lane >> 1)] = 0.f;
+            }
+            const int tile = (c0 >> 6) * ATOM;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t off = swz(row, (c0 & 63) * 2 + j * 16);
+                *reinterpret_cast<uint4 *>(sm + L_::P + tile + off) = make_uint4(pb[4 * j], pb[4 * j + 1], pb[4 * j + 2], pb[4 * j + 3]);
+                *reinterpret_cast<uint4 *>(sm + L_::DA + tile + off) = make_uint4(ab[4 * j], ab[4 * j + 1], ab[4 * j + 2], ab[4 * j + 3]);
+            }
+        }
+        zr[cg * C + row] = z;
+    }
+    // ---- the states' parts of dQ and dK: dot products with q and k, rows scaled in place
+    if (cg < 2 * KATOMS) {
+        const float fa = a.scale * since, fw = until;
+        float xs = 0.f, ys = 0.f;
+#pragma unroll 1
+        for (int p = 0; p < 32; p += 16) {
+            const int c0 = cg * 32 + p;
+            float x[16], y[16];
+            tmem_ld16x2(T_DQ + lanes + c0, T_DK + lanes + c0, x, y);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t off = (c0 >> 6) * ATOM + swz(row, (c0 & 63) * 2 + j * 16);
+                const uint4 qv = *reinterpret_cast<const uint4 *>(sm + L_::Q + off), kv = *reinterpret_cast<const uint4 *>(sm + L_::K + off);
+                const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, kw[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    xs = fmaf(bf16_lo(qw[i]), x[8 * j + 2 * i], xs);
+                    xs = fmaf(bf16_hi(qw[i]), x[8 * j + 2 * i + 1], xs);
+                    ys = fmaf(bf16_lo(kw[i]), y[8 * j + 2 * i], ys);
+                    ys = fmaf(bf16_hi(kw[i]), y[8 * j + 2 * i + 1], ys);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                x[j] *= fa;
+                y[j] *= fw;
+            }
+            tmem_st16(T_DQ + lanes + c0, x);
+            tmem_st16(T_DK + lanes + c0, y);
+        }
+        xi[cg * C + row] = fa * xs;
+        yi[cg * C + row] = fw * ys;
+    }
+    sr = warp_sum(sr);
+    if (lane == 0) sr_w[warp] = sr;
+    publish();
+
+    // ---- the rest of the products, for the resident (last) half of d_v
+    const int last = (tiles - 1) & ~1;
+    auto value_parts = [&]() {                // P^T dO into the scores' columns, K R into dP's
+        if (nt == 2) {
+            mma_tiles<8, true, true, 128>(T_SC, sb + L_::P, sb + L_::DO, false);
+            mma_tiles<4 * KATOMS, false, true, 128>(T_DP, sb + L_::K, sb + L_::R1, false);
+        } else {
+            mma_tiles<8, true, true, 64>(T_SC, sb + L_::P, sb + L_::DO, false);
+            mma_tiles<4 * KATOMS, false, true, 64>(T_DP, sb + L_::K, sb + L_::R1, false);
+        }
+    };
+    if (one) {
+        mma_tiles<8, false, true, NK>(T_DQ, sb + L_::DA, sb + L_::K, true);
+        mma_tiles<8, true, true, NK>(T_DK, sb + L_::DA, sb + L_::Q, true);
+        value_parts();
+        mma_commit(bar_mma);
+    }
+    // meanwhile one warp sums up the decay's gradient, four tokens per lane
+    if (f.b.dg && warp == 1) {
+        float s0 = 0.f;
+        for (int i = 0; i < NT / 32; ++i) s0 += sr_w[i];
+        const float whole = d.whole.x * s0;
+        Log2 later[4], earlier[4];            // sums in two floats, as for the decays
+        for (int e = 0; e < 4; ++e) {
+            const int t = lane * 4 + e;
+            float rows = 0.f, cols = 0.f, x = 0.f, y = 0.f;
+            for (int i = 0; i < 4; ++i) {
+                rows += zr[i * C + t];
+                cols += zc[i * C + t];
+                if (i < 2 * KATOMS) {
+                    x += xi[i * C + t];
+                    y += yi[i * C + t];
+                }
+            }
+            later[e] = Log2{rows, x} + Log2{-cols, 0.f};
+            earlier[e] = {y, 0.f};
+        }
+        Log2 sl = (later[0] + later[1]) + (later[2] + later[3]), se = (earlier[0] + earlier[1]) + (earlier[2] + earlier[3]);
+        Log2 fl = sl, fe = se;
+        for (int off = 1; off < 32; off <<= 1) {
+            const Log2 yl = {__shfl_down_sync(0xffffffffu, fl.hi, off), __shfl_down_sync(0xffffffffu, fl.lo, off)};
+            const Log2 ye = {__shfl_up_sync(0xffffffffu, fe.hi, off), __shfl_up_sync(0xffffffffu, fe.lo, off)};
+            if (lane + off < 32) fl = fl + yl;
+            if (lane >= off) fe = fe + ye;
+        }
+        Log2 after = fl - sl, before = fe - se;   // the lanes' above, below
+        float g[4];
+        for (int e = 3; e >= 0; --e) {
+            after = after + later[e];
+            g[e] = after.hi;
+        }
+        float sum = 0.f;
+        for (int e = 0; e < 4; ++e) {
+            g[e] = (g[e] + before.hi) + whole;
+            before = before + earlier[e];
+            const int t = lane * 4 + e;
+            if (t < L) {
+                sum += g[e];
+                if (a.decay == KDN_DECAY_TOKEN) f.b.dg[(size_t)(tok + t) * a.H + h] = g[e];
+            }
+        }
+        if (a.decay == KDN_DECAY_HEAD) {
+            sum = warp_sum(sum);
+            if (lane == 0) f.s.share[(size_t)u * a.H + h] = sum;
+        }
+    }
+    wait_mma();
+
+    // ---- out: 32 columns of a warp's 32 rows at a time through shared memory that no MMA reads any more, so that four
+    // lanes share a row's 64 bytes in memory
+    auto put = [&](bf16 *dst, int width, int col, int tile, const float (&x)[32]) {
+        if (col >= width) return;
+        const int base = tile + (col >> 6) % 2 * ATOM;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = round_bf16x2(pk2(x[8 * j + 2 * i], x[8 * j + 2 * i + 1]));
+            *reinterpret_cast<uint4 *>(sm + base + swz(row, (col & 63) * 2 + j * 16)) = make_uint4(z[0], z[1], z[2], z[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 32; r += 8) {
+            const int t = q4 * 32 + r + (lane >> 2);
+            const uint4 z = *reinterpret_cast<const uint4 *>(sm + base + swz(t, (col & 63) * 2 + (lane & 3) * 16));
+            if (t < L) *reinterpret_cast<uint4 *>(dst + ((size_t)(tok + t) * a.H + h) * width + col + (lane & 3) * 8) = z;
+        }
+        __syncwarp();
+    };
+    auto put_values = [&](int t0) {
+        if (cg < 2 * nt) {
+            float x[32], y[32];
+            tmem_ld32(T_SC + lanes + cg * 32, x);
+            tmem_ld32(T_DP + lanes + cg * 32, y);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = fmaf(until, y[j], x[j]);
+            put(static_cast<bf16 *>(f.b.dv), a.dv, t0 * DVT + cg * 32, L_::DO, x);
+        }
+    };
+    if (cg < 2 * KATOMS) {
+        float x[32];
+        tmem_ld32(T_DQ + lanes + cg * 32, x);
+        put(static_cast<bf16 *>(f.b.dq), a.dk, cg * 32, tiles > 2 ? L_::DA : L_::Q, x);   // K and P are read once more for the first half
+        tmem_ld32(T_DK + lanes + cg * 32, x);
+        put(static_cast<bf16 *>(f.b.dk), a.dk, cg * 32, tiles > 2 ? L_::DA : L_::Q, x);
+    }
+    put_values(last);
+    // ---- the first half's dV (d_v = 256)
+    for (int t0 = last - 2; t0 >= 0; t0 -= 2) {
+        publish();                            // the tiles that were written through are read, TMEM too
+        load_half(t0, false);
+        for (int t = 0; t < nt; ++t) {
+            fetch(f.s.R, t0 + t, R);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float4 y0 = R[2 * j], y1 = R[2 * j + 1];
+                *reinterpret_cast<uint4 *>(sm + L_::R1 + t * ATOM + swz(row, (cg * 2 + j) * 16)) =
+                    make_uint4(round_bf16x2(pk2(y0.x, y0.y)), round_bf16x2(pk2(y0.z, y0.w)), round_bf16x2(pk2(y1.x, y1.y)), round_bf16x2(pk2(y1.z, y1.w)));
+            }
+        }
+        wait_tma();
+        zero_tail(L_::DO, nt);
+        publish();
+        if (one) {
+            value_parts();
+            mma_commit(bar_mma);
+        }
+        wait_mma();
+        put_values(t0);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {                        // a wait gave up: bounded waits for what is in flight, before its memory goes
+        if (threadIdx.x == 0) {
+            raise_error(a.err, ERR_TIMEOUT);
+            drain(bar_tma, 0);
+            drain(bar_tma, 1);
+        }
+        if (one) {
+            mbar_init(bar_mma, 1);
+            mbar_fence_init();
+            mma_commit(bar_mma);
+            drain(bar_mma, 0);
+        }
+        __syncthreads();
+    }
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+size_t linear_tc_backward_workspace_bytes(const LinArgs &a) { return states_workspace_bytes(a); }
+
+cudaError_t launch_linear_tc_backward(const LinBwdArgs &b, void *workspace, cudaStream_t st) {
+    const LinArgs &a = b.a;
+    GradArgs f;
+    f.b = b;
+    cudaError_t e = launch_states(b, workspace, &f.s, st);
+    if (e != cudaSuccess) return e;
+    if (!make_token_map(&f.tq, a.q, a.dk, a.H, a.ntok) || !make_token_map(&f.tk, a.k, a.dk, a.H, a.ntok) ||
+        !make_token_map(&f.tv, a.v, a.dv, a.H, a.ntok) || !make_token_map(&f.to, b.d_o, a.dv, a.H, a.ntok))
+        return cudaErrorInvalidValue;
+    auto kern = a.dk > 64 ? linear_grad_tc_kernel<2> : linear_grad_tc_kernel<1>;
+    KernelSetup ks;
+    e = kernel_setup(reinterpret_cast<const void *>(kern), Smem::TOTAL, NT, false, &ks);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(lin_slots(a.cu != nullptr, a.T, a.ntok, a.nseq, C) * a.H), NT, Smem::TOTAL, st>>>(f);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !b.dg || a.decay != KDN_DECAY_HEAD) return e;
+    return launch_linear_head_decay(a, f.s.share, b.dg, C, st);
+}
+
+}  // namespace kdn

@@ -435,6 +435,11 @@ __global__ void __launch_bounds__(256) linear_head_decay_kernel(LinArgs a, const
 }
 
 // ------------------------------------------------------------------ host side
+cudaError_t launch_linear_head_decay(const LinArgs &a, const float *share, float *dg, int tokens, cudaStream_t st) {
+    linear_head_decay_kernel<<<a.H, 256, 0, st>>>(a, share, dg, (int)lin_slots(a.cu != nullptr, a.T, a.ntok, a.nseq, tokens), tokens);
+    return cudaGetLastError();
+}
+
 namespace {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -497,8 +502,7 @@ cudaError_t backward(const LinBwdArgs &b, uint8_t *wsp, cudaStream_t st) {
     kern<<<(unsigned)(slots_of(a) * a.H), NT, smem, st>>>(b, ws);
     e = cudaGetLastError();
     if (e != cudaSuccess || !b.dg || a.decay != KDN_DECAY_HEAD) return e;
-    linear_head_decay_kernel<<<a.H, 256, 0, st>>>(a, ws.dgc, b.dg, (int)slots_of(a), C);
-    return cudaGetLastError();
+    return launch_linear_head_decay(a, ws.dgc, b.dg, C, st);
 }
 
 #define KDN_LINEAR_SIZES(FN, ARG)                                                                              \

@@ -122,19 +122,10 @@ __device__ __forceinline__ void add_delta(f32x2 (&S)[16], uint32_t d, float2 dec
     }
 }
 
-// thread 0 of the TMA warp: a [128 tokens][64 channels] tile as two boxes of 64 tokens
-__device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, int c0, int h, int tok, uint64_t *bar) {
-    tma_load_3d(dst, m, c0, h, tok, bar);
-    tma_load_3d(dst + ATOM / 2, m, c0, h, tok + 64, bar);
-}
-
 __device__ __forceinline__ void prefetch_tile(const CUtensorMap *m, int c0, int h, int tok) {
     tma_prefetch_3d(m, c0, h, tok);
     tma_prefetch_3d(m, c0, h, tok + 64);
 }
-
-// after a wait gave up: one more bounded wait for a barrier that copies or MMAs in flight still arrive on
-__device__ __noinline__ void drain(uint64_t *bar, uint32_t parity) { mbar_wait(bar, parity, 100000000ll); }
 
 }  // namespace
 
@@ -766,5 +757,53 @@ cudaError_t launch_linear_tc(const LinArgs &a, void *workspace, cudaStream_t st)
     kern<<<(unsigned)(slots(a, f.sp.seg) * a.H * tiles_of(a)), NT_F, FwdSmem::TOTAL, st>>>(f);
     return cudaGetLastError();
 }
+
+namespace lin {
+
+size_t states_workspace_bytes(const LinArgs &a) {
+    int seg, sub;
+    split_of(a, &seg, &sub);
+    const size_t n = (size_t)slots(a, C) * a.H;
+    return decay_bytes(a) + (is_split(a, seg) ? totals_bytes(a, sub) : 0) + 2 * round256(n * tiles_of(a) * TILE_FLOATS * 4) + round256(n * 4);
+}
+
+cudaError_t launch_states(const LinBwdArgs &b, void *workspace, States *out, cudaStream_t st) {
+    const LinArgs &a = b.a;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    int seg, sub;
+    split_of(a, &seg, &sub);
+    const size_t n = (size_t)slots(a, C) * a.H, tile_bytes = round256(n * tiles_of(a) * TILE_FLOATS * 4);
+    uint8_t *tot = ws + decay_bytes(a);
+    float *S = reinterpret_cast<float *>(tot + (is_split(a, seg) ? totals_bytes(a, sub) : 0)), *R = S + tile_bytes / 4;
+    out->decay = static_cast<const Decay *>(workspace);
+    out->S = S;
+    out->R = R;
+    out->share = R + tile_bytes / 4;
+    cudaError_t e = decays(a, workspace, st);
+    if (e != cudaSuccess) return e;
+    StateArgs f{};
+    f.a = a;
+    f.decay = out->decay;
+    // forwards: the states at the chunks' starts
+    if (!make_token_map(&f.tx, a.k, a.dk, a.H, a.ntok) || !make_token_map(&f.ty, a.v, a.dv, a.H, a.ntok)) return cudaErrorInvalidValue;
+    e = totals<false>(f, tot, &f.sp, st);
+    if (e != cudaSuccess) return e;
+    f.piece = f.sp.seg;
+    f.tiles = S;
+    f.first = a.S0;
+    e = states<false, false>(f, st);
+    if (e != cudaSuccess) return e;
+    // backwards: the state's gradient at their ends
+    if (!make_token_map(&f.tx, a.q, a.dk, a.H, a.ntok) || !make_token_map(&f.ty, b.d_o, a.dv, a.H, a.ntok)) return cudaErrorInvalidValue;
+    e = totals<true>(f, tot, &f.sp, st);
+    if (e != cudaSuccess) return e;
+    f.piece = f.sp.seg;
+    f.tiles = R;
+    f.first = b.dS_T;
+    f.last = b.dS0;
+    return states<true, false>(f, st);
+}
+
+}  // namespace lin
 
 }  // namespace kdn

@@ -21,7 +21,7 @@ constexpr int ATOM = C * 128;      // bytes of a [128 rows][64 bf16] swizzled ti
 // kernels then stop issuing work and drain what is in flight.
 // (The slow path is a call, the hot loops are kept rolled and the sizes template arguments: the roles of a
 // kernel run side by side, and together they have to stay in the instruction cache.)
-__device__ __noinline__ bool wait_slowly(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+static __device__ __noinline__ bool wait_slowly(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
     const long long t0 = clock64();
     while (!mbar_try_wait_for(bar, parity, 1000000u)) {
         if (*abort_flag) return false;
@@ -153,6 +153,23 @@ constexpr size_t TILE_FLOATS = 128 * 64;
 __device__ __forceinline__ size_t tile_at(size_t slot, int H, int h, int tiles, int tile) {
     return ((slot * H + h) * tiles + tile) * TILE_FLOATS;
 }
+
+// thread of a TMA issuer: a [128 tokens][64 channels] tile as two boxes of 64 tokens
+__device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, int c0, int h, int tok, uint64_t *bar) {
+    tma_load_3d(dst, m, c0, h, tok, bar);
+    tma_load_3d(dst + ATOM / 2, m, c0, h, tok + 64, bar);
+}
+// after a wait gave up: one more bounded wait for a barrier that copies or MMAs in flight still arrive on
+static __device__ __noinline__ void drain(uint64_t *bar, uint32_t parity) { mbar_wait(bar, parity, 100000000ll); }
+
+// What the backward's first launches leave in the workspace for its last one
+struct States {
+    const Decay *decay;            // [slots of C][H]
+    const float *S, *R;            // [slots of C][H][tiles]: states at the chunks' starts, state gradients at their ends
+    float *share;                  // [slots of C][H]: the chunks' shares of a per-head decay's gradient
+};
+size_t states_workspace_bytes(const LinArgs &a);
+cudaError_t launch_states(const LinBwdArgs &b, void *workspace, States *out, cudaStream_t st);
 
 }  // namespace lin
 }  // namespace kdn
