@@ -11,6 +11,8 @@
 // two parts of dV.  Rounding: P and dA, and R in K R, are bf16 (dq, dk and dv are); S and R enter the
 // products that dg is summed from as three bf16 terms, so dg keeps fp32's accuracy.
 // Per chunk and head at d = 128: 12 products of 128 x 128 x 128 (6100 cycles of MMA), 352 KB in and 96 KB out.
+#include <type_traits>
+
 #include "kdn_launch.h"
 #include "kdn_linear_tc.cuh"
 
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = __ldg(reinterpret_cast<const float4 *>(tile + ((cg * 4 + j) * 128 + row) * 4));
     };
-    auto terms = [&](const float4 (&x)[4], int p0, int p1, int p2) {
+    auto terms = [&](const float4 (&x)[4], auto rounded, int p0, int p1, int p2) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint32_t o[3][4];
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             for (int i = 0; i < 4; ++i) {
                 const float4 y = x[2 * j + (i >> 1)];
                 uint32_t t[3];
-                split3(i & 1 ? pk2(y.z, y.w) : pk2(y.x, y.y), t);
+                split3<decltype(rounded)::value>(i & 1 ? pk2(y.z, y.w) : pk2(y.x, y.y), t);
                 o[0][i] = t[0]; o[1][i] = t[1]; o[2][i] = t[2];
             }
             const uint32_t off = swz(row, (cg * 2 + j) * 16);
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
         zero_tail(L_::V, nt);
         zero_tail(L_::DO, nt);
         for (int t = 0; t < nt; ++t) {
-            terms(S, L_::ST, L_::ST + ATOM, L_::ST + 2 * ATOM);
+            terms(S, std::false_type(), L_::ST, L_::ST + ATOM, L_::ST + 2 * ATOM);
             fetch(f.s.R, t0 + t, R);
             publish();
             if (one) {
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
                 sr += S[j].x * R[j].x + S[j].y * R[j].y + S[j].z * R[j].z + S[j].w * R[j].w;
             if (t0 + t + 1 < tiles) fetch(f.s.S, t0 + t + 1, S);
             wait_mma();
-            terms(R, L_::R1 + t * ATOM, L_::ST + ATOM, L_::ST + 2 * ATOM);
+            terms(R, std::true_type(), L_::R1 + t * ATOM, L_::ST + ATOM, L_::ST + 2 * ATOM);
             publish();
             if (one) {
                 mma_tiles<4, false, false, NK>(T_DK, sb + L_::V + t * ATOM, sb + L_::R1 + t * ATOM, t0 + t > 0);

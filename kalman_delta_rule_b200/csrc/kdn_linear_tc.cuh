@@ -81,13 +81,6 @@ __device__ __forceinline__ uint32_t upper_halves(f32x2 x) {   // two bf16 by tru
     return __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
 }
 __device__ __forceinline__ f32x2 trunc2(f32x2 x) { return x & 0xffff0000ffff0000ull; }
-__device__ __forceinline__ void split3(f32x2 x, uint32_t (&t)[3]) {
-    t[0] = upper_halves(x);
-    x = sub2(x, trunc2(x));
-    t[1] = upper_halves(x);
-    x = sub2(x, trunc2(x));
-    t[2] = upper_halves(x);
-}
 // two fp32 rounded to nearest bf16 on the FMA pipe: with c = (2^16 + 1) x, c - (c - x) has the leading 8
 // bits (Veltkamp's splitting; beyond 2^111 the result is not a number, as for an infinity).  c is a rounded fma:
 // a packed product may be contracted with the subtraction, which would undo the rounding it is there for.
@@ -96,6 +89,16 @@ __device__ __forceinline__ uint32_t round_bf16x2(f32x2 x) {
     return upper_halves(sub2(c, sub2(c, x)));
 }
 
+// ROUND: the first term rounded to nearest (the rest may then be negative; it still has 16 bits), for terms of
+// which the first serves alone somewhere
+template <bool ROUND = false>
+__device__ __forceinline__ void split3(f32x2 x, uint32_t (&t)[3]) {
+    t[0] = ROUND ? round_bf16x2(x) : upper_halves(x);
+    x = sub2(x, ROUND ? unpack2(t[0]) : trunc2(x));
+    t[1] = upper_halves(x);
+    x = sub2(x, trunc2(x));
+    t[2] = upper_halves(x);
+}
 // half a row of a [128][64] bf16 tile, weighted, as three terms in three tiles (thread = row x half)
 __device__ __forceinline__ void weigh_row(const uint8_t *src, uint8_t *dst, int row, int half, float w) {
 #pragma unroll 2
