@@ -43,7 +43,7 @@ static_assert(FwdSmem::TOTAL <= 227 * 1024, "shared memory");
 
 struct StateSmem {
     static constexpr int X = 0, Y = X + 2 * 2 * ATOM, VP = Y + 2 * ATOM, DEC = VP + 2 * 3 * ATOM,
-                         BAR = DEC + 2 * (int)sizeof(Decay), NBAR = 14,
+                         BAR = DEC + 2 * (int)sizeof(Decay), NBAR = 18,
                          CTL = BAR + NBAR * 8, TOTAL = CTL + 16;
 };
 static_assert(StateSmem::TOTAL <= 227 * 1024, "shared memory");
@@ -507,8 +507,8 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
     const int c0 = lin_first_slot(a, pc.s, pc.t0, C) + pc.j * (f.piece / C);   // the piece's first chunk's slot
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L_::BAR);
-    uint64_t *full = bar, *empty = bar + 2, *vp_full = bar + 4, *dl_full = bar + 6, *dl_free = bar + 8, *dec_full = bar + 10,
-             *dec_empty = bar + 12;
+    uint64_t *x_full = bar, *x_free = bar + 2, *y_full = bar + 4, *y_free = bar + 6, *vp_full = bar + 8, *dl_full = bar + 10,
+             *dl_free = bar + 12, *dec_full = bar + 14, *dec_empty = bar + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L_::CTL);
     int *abort_flag = reinterpret_cast<int *>(sm + L_::CTL + 4);
     const Waits w{abort_flag};
@@ -516,8 +516,10 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, 1);
+            mbar_init(x_full + i, 1);
+            mbar_init(x_free + i, 1);
+            mbar_init(y_full + i, 1);
+            mbar_init(y_free + i, NW_W);
             mbar_init(vp_full + i, NW_W);
             mbar_init(dl_full + i, 1);
             mbar_init(dl_free + i, NW_S);
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
         const int vrow = threadIdx.x & 127, vhalf = threadIdx.x >> 7;
         for (int c = 0; c < n; ++c) {
             const int st = c & 1, L = min(C, len - chunk(c) * C);
-            if (!w.wait(dec_full + st, (c >> 1) & 1) || !w.wait(full + st, (c >> 1) & 1)) break;
+            if (!w.wait(dec_full + st, (c >> 1) & 1) || !w.wait(y_full + st, (c >> 1) & 1)) break;
             if (c >= 2 && !w.wait(dl_full + st, ((c >> 1) - 1) & 1)) break;   // the MMAs that read this buffer
             uint8_t *vp = sm + L_::VP + st * 3 * ATOM;
             if (vrow < L) {
@@ -556,10 +558,11 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
             } else {
 #pragma unroll
                 for (int k = 0; k < 3; ++k) zero_row(vp + k * ATOM, vrow, vhalf * 4, 4);
-                zero_row(sm + L_::X + (st * 2 + vhalf) * ATOM, vrow, 0, 8);
+                if (w.wait(x_full + st, (c >> 1) & 1)) zero_row(sm + L_::X + (st * 2 + vhalf) * ATOM, vrow, 0, 8);
             }
             fence_async_smem();
             warp_arrive(vp_full + st);
+            warp_arrive(y_free + st);
             warp_arrive(dec_empty + st);
         }
     } else if (warp < W_MMA) {
@@ -606,27 +609,35 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
         if (lane == 0) {
             for (int c = 0; c < n; ++c) {
                 const int st = c & 1, tok = tok0 + chunk(c) * C;
-                if (c >= 2 && !w.wait(empty + st, ((c >> 1) - 1) & 1)) break;
+                if (c + 2 < n) {              // (as in the forward)
+                    const int far = tok0 + chunk(c + 2) * C;
+                    for (int k = 0; k < KATOMS; ++k) prefetch_tile(&f.tx, k * 64, h, far);
+                    prefetch_tile(&f.ty, tile * DVT, h, far);
+                }
+                const uint32_t before = ((c >> 1) - 1) & 1;
+                if (c >= 2 && !w.wait(dec_empty + st, before)) break;
                 if (*w.abort_flag) break;
-                mbar_expect_tx(full + st, (uint32_t)(KATOMS + 1) * ATOM);
-                if (c >= 2 && !w.wait(dec_empty + st, ((c >> 1) - 1) & 1)) break;
                 mbar_expect_tx(dec_full + st, sizeof(Decay));
                 bulk_load(dec + st, f.decay + (size_t)(c0 + chunk(c)) * a.H + h, sizeof(Decay), dec_full + st);
-                for (int k = 0; k < KATOMS; ++k) load_tile(sm + L_::X + (st * 2 + k) * ATOM, &f.tx, k * 64, h, tok, full + st);
-                load_tile(sm + L_::Y + st * ATOM, &f.ty, tile * DVT, h, tok, full + st);
+                if (c >= 2 && !w.wait(y_free + st, before)) break;      // (read once, early: refilled a good chunk ahead)
+                mbar_expect_tx(y_full + st, ATOM);
+                load_tile(sm + L_::Y + st * ATOM, &f.ty, tile * DVT, h, tok, y_full + st);
+                if (c >= 2 && !w.wait(x_free + st, before)) break;
+                mbar_expect_tx(x_full + st, (uint32_t)KATOMS * ATOM);
+                for (int k = 0; k < KATOMS; ++k) load_tile(sm + L_::X + (st * 2 + k) * ATOM, &f.tx, k * 64, h, tok, x_full + st);
             }
         }
     } else if (warp == W_MMA) {
         const bool one = elect_one();
         for (int c = 0; c < n; ++c) {
             const int st = __shfl_sync(0xffffffffu, c & 1, 0);
-            if (!w.wait(full + st, (c >> 1) & 1) || !w.wait(vp_full + st, (c >> 1) & 1)) break;
+            if (!w.wait(x_full + st, (c >> 1) & 1) || !w.wait(vp_full + st, (c >> 1) & 1)) break;
             if (c >= 2 && !w.wait(dl_free + st, ((c >> 1) - 1) & 1)) break;
             tc_fence_after();
             if (one) {
                 mma_delta(tmem + st * 192, sb + L_::X + st * 2 * ATOM, sb + L_::VP + st * 3 * ATOM);
                 mma_commit(dl_full + st);
-                mma_commit(empty + st);
+                mma_commit(x_free + st);
             }
         }
     }
@@ -638,7 +649,8 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
             raise_error(a.err, ERR_TIMEOUT);
             for (int i = 0; i < 2; ++i) {
                 for (uint32_t ph = 0; ph < 2; ++ph) {
-                    drain(full + i, ph);
+                    drain(x_full + i, ph);
+                    drain(y_full + i, ph);
                     drain(dec_full + i, ph);
                 }
             }
