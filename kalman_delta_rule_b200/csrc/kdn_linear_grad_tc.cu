@@ -23,11 +23,13 @@ using namespace lin;
 namespace {
 
 constexpr int NT = 512;
+constexpr int SMS = 148;
 
 struct Smem {
     static constexpr int Q = 0, K = Q + 2 * ATOM, DO = K + 2 * ATOM, V = DO + 2 * ATOM, ST = V + 2 * ATOM, R1 = ST + 3 * ATOM,
-                         DEC = R1 + 2 * ATOM, SUM = DEC + (int)sizeof(Decay), CTL = SUM + (4 * 4 * C + 32) * 4, TOTAL = CTL + 32;
+                         DEC = R1 + 2 * ATOM, SUM = DEC + (int)sizeof(Decay), CTL = SUM + (4 * 4 * C + 32) * 4, TOTAL = CTL + 48;
     static constexpr int P = ST, DA = V;      // once the states' terms and V have been used
+    static constexpr int R2 = Q;              // the second and third terms of R, between the scores and the second load of q
 };
 static_assert(Smem::TOTAL <= 227 * 1024, "shared memory");
 
@@ -70,8 +72,8 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     const int row = q4 * 32 + lane;
     const uint32_t lanes = ((uint32_t)q4 * 32u) << 16;
 
-    uint64_t *bar_tma = reinterpret_cast<uint64_t *>(sm + L_::CTL), *bar_mma = bar_tma + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_mma + 1);
+    uint64_t *bar_tma = reinterpret_cast<uint64_t *>(sm + L_::CTL), *bar_a = bar_tma + 1, *bar_b = bar_tma + 2, *bar_c = bar_tma + 3;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_tma + 4);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
     const Waits w{abort_flag};
     const Decay &d = *reinterpret_cast<const Decay *>(sm + L_::DEC);
@@ -79,7 +81,9 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
 
     if (threadIdx.x == 0) {
         mbar_init(bar_tma, 1);
-        mbar_init(bar_mma, 1);
+        mbar_init(bar_a, 1);
+        mbar_init(bar_b, 1);
+        mbar_init(bar_c, 1);
         mbar_fence_init();
         *abort_flag = (sb & 1023u) ? 1 : 0;
     }
@@ -91,28 +95,18 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     const uint32_t T_SC = tmem, T_DP = tmem + 128, T_DQ = tmem + 256, T_DK = tmem + 384;
     const bool one = warp == 0 && elect_one();
     // every thread takes every wait and every barrier; after a wait that gave up the rest give up at once
-    uint32_t ph_tma = 0, ph_mma = 0;
+    uint32_t ph_tma = 0, ph_a = 0, ph_b = 0;  // MMAs are committed to two barriers in turn
     auto wait_tma = [&]() { w.wait(bar_tma, ph_tma); ph_tma ^= 1; };
-    auto wait_mma = [&]() { w.wait(bar_mma, ph_mma); ph_mma ^= 1; tc_fence_after(); };
+    auto wait_a = [&]() { w.wait(bar_a, ph_a); ph_a ^= 1; tc_fence_after(); };
+    auto wait_b = [&]() { w.wait(bar_b, ph_b); ph_b ^= 1; tc_fence_after(); };
     auto publish = [&]() {                    // this thread's shared-memory and TMEM work, before the next MMAs
         fence_async_smem();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
     };
-    auto load_half = [&](int t0, bool first) {
-        if (threadIdx.x == 0) {
-            mbar_expect_tx(bar_tma, (uint32_t)((first ? 2 * KATOMS + nt : 0) + nt) * ATOM + (first ? (uint32_t)sizeof(Decay) : 0u));
-            if (first) {
-                bulk_load(sm + L_::DEC, f.s.decay + (size_t)u * a.H + h, sizeof(Decay), bar_tma);
-                for (int k = 0; k < KATOMS; ++k) {
-                    load_tile(sm + L_::Q + k * ATOM, &f.tq, k * 64, h, tok, bar_tma);
-                    load_tile(sm + L_::K + k * ATOM, &f.tk, k * 64, h, tok, bar_tma);
-                }
-                for (int t = 0; t < nt; ++t) load_tile(sm + L_::V + t * ATOM, &f.tv, (t0 + t) * DVT, h, tok, bar_tma);
-            }
-            for (int t = 0; t < nt; ++t) load_tile(sm + L_::DO + t * ATOM, &f.to, (t0 + t) * DVT, h, tok, bar_tma);
-        }
+    auto load = [&](const CUtensorMap *m, int region, int c0, int n) {   // (thread 0)
+        for (int t = 0; t < n; ++t) load_tile(sm + region + t * ATOM, m, c0 + t * 64, h, tok, bar_tma);
     };
     // 16 columns of a state tile's row in registers, and as terms in shared memory
     auto fetch = [&](const float *base, int t, float4 (&x)[4]) {
@@ -142,61 +136,99 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             for (int t = 0; t < n; ++t) zero_row(sm + tile + t * ATOM, row, cg * 2, 2);
     };
 
-    // ---- products with the states, half of d_v (two tiles) after half; the scores in the first one
+    if (threadIdx.x == 0) {
+        mbar_expect_tx(bar_tma, (uint32_t)(2 * KATOMS + 2 * nt) * ATOM + (uint32_t)sizeof(Decay));
+        bulk_load(sm + L_::DEC, f.s.decay + (size_t)u * a.H + h, sizeof(Decay), bar_tma);
+        load(&f.tq, L_::Q, 0, KATOMS);
+        load(&f.tk, L_::K, 0, KATOMS);
+        load(&f.to, L_::DO, 0, nt);
+        load(&f.tv, L_::V, 0, nt);
+    }
+    // ---- products with the states, tile after tile of d_v (two are resident); the scores with the first.  The terms of
+    // the next operand are formed while the products of the one before run: S's in ST, R's in R1 and where q was
     float sr = 0.f;
     float4 S[4], R[4];
-    for (int t0 = 0; t0 < tiles; t0 += 2) {
-        if (t0 == 0) {
-            load_half(0, true);
-            fetch(f.s.S, 0, S);
-        } else if (threadIdx.x == 0) {        // (the products that read the first half's tiles were waited for)
-            mbar_expect_tx(bar_tma, (uint32_t)(2 * nt) * ATOM);
-            for (int t = 0; t < nt; ++t) {
-                load_tile(sm + L_::V + t * ATOM, &f.tv, (t0 + t) * DVT, h, tok, bar_tma);
-                load_tile(sm + L_::DO + t * ATOM, &f.to, (t0 + t) * DVT, h, tok, bar_tma);
-            }
-        }
-        wait_tma();
-        if (t0 == 0) {
-            zero_tail(L_::Q, KATOMS);
-            zero_tail(L_::K, KATOMS);
-        }
-        zero_tail(L_::V, nt);
-        zero_tail(L_::DO, nt);
-        for (int t = 0; t < nt; ++t) {
-            terms(S, std::false_type(), L_::ST, L_::ST + ATOM, L_::ST + 2 * ATOM);
-            fetch(f.s.R, t0 + t, R);
-            publish();
-            if (one) {
-                if (t == 0) {
-                    if (t0 == 0) mma_tiles<4 * KATOMS, false, false, 128>(T_SC, sb + L_::Q, sb + L_::K, false);
-                    for (int i = 0; i < nt; ++i) mma_tiles<4, false, false, 128>(T_DP, sb + L_::DO + i * ATOM, sb + L_::V + i * ATOM, t0 + i > 0);
+    fetch(f.s.S, 0, S);
+    fetch(f.s.R, 0, R);
+    for (int t = 0; t < tiles; ++t) {
+        const int i = t & 1;
+        if (i == 0) {
+            if (t > 0) {                      // the second half: nothing reads the first one's tiles any more
+                wait_b();
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    mbar_expect_tx(bar_tma, (uint32_t)(2 * nt) * ATOM);
+                    load(&f.to, L_::DO, t * DVT, nt);
+                    load(&f.tv, L_::V, t * DVT, nt);
                 }
-#pragma unroll 1
-                for (int p = 0; p < 3; ++p) mma_tiles<4, false, false, NK>(T_DQ, sb + L_::DO + t * ATOM, sb + L_::ST + p * ATOM, t0 + t + p > 0);
-                mma_commit(bar_mma);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                sr += S[j].x * R[j].x + S[j].y * R[j].y + S[j].z * R[j].z + S[j].w * R[j].w;
-            if (t0 + t + 1 < tiles) fetch(f.s.S, t0 + t + 1, S);
-            wait_mma();
-            terms(R, std::true_type(), L_::R1 + t * ATOM, L_::ST + ATOM, L_::ST + 2 * ATOM);
-            publish();
-            if (one) {
-                mma_tiles<4, false, false, NK>(T_DK, sb + L_::V + t * ATOM, sb + L_::R1 + t * ATOM, t0 + t > 0);
-#pragma unroll 1
-                for (int p = 1; p < 3; ++p) mma_tiles<4, false, false, NK>(T_DK, sb + L_::V + t * ATOM, sb + L_::ST + p * ATOM, true);
-                mma_commit(bar_mma);
+            wait_tma();
+            if (t == 0) {
+                zero_tail(L_::Q, KATOMS);
+                zero_tail(L_::K, KATOMS);
             }
-            wait_mma();
+            zero_tail(L_::V, nt);
+            zero_tail(L_::DO, nt);
         }
+        if (t > 0) wait_a();
+        terms(S, std::false_type(), L_::ST, L_::ST + ATOM, L_::ST + 2 * ATOM);
+        publish();
+        if (one) {
+            if (t == 0) {
+                mma_tiles<4 * KATOMS, false, false, 128>(T_SC, sb + L_::Q, sb + L_::K, false);
+                mma_commit(bar_b);
+            }
+#pragma unroll 1
+            for (int p = 0; p < 3; ++p) mma_tiles<4, false, false, NK>(T_DQ, sb + L_::DO + i * ATOM, sb + L_::ST + p * ATOM, t + p > 0);
+            mma_tiles<4, false, false, 128>(T_DP, sb + L_::DO + i * ATOM, sb + L_::V + i * ATOM, t > 0);
+            mma_commit(bar_a);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sr += S[j].x * R[j].x + S[j].y * R[j].y + S[j].z * R[j].z + S[j].w * R[j].w;
+        if (t + 1 < tiles) fetch(f.s.S, t + 1, S);
+        if (i == 1 || t == 0) wait_b();       // the scores (q's place is free), or the products of R's terms before
+        terms(R, std::true_type(), L_::R1 + i * ATOM, L_::R2, L_::R2 + ATOM);
+        publish();
+        if (one) {
+            mma_tiles<4, false, false, NK>(T_DK, sb + L_::V + i * ATOM, sb + L_::R1 + i * ATOM, t > 0);
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p) mma_tiles<4, false, false, NK>(T_DK, sb + L_::V + i * ATOM, sb + L_::R2 + p * ATOM, true);
+            mma_commit(bar_b);
+        }
+        if (t + 1 < tiles) fetch(f.s.R, t + 1, R);
+    }
+    wait_a();
+    wait_b();
+    if (threadIdx.x == 0) {                   // q again (from L2)
+        mbar_expect_tx(bar_tma, (uint32_t)KATOMS * ATOM);
+        load(&f.tq, L_::Q, 0, KATOMS);
     }
 
+    if (threadIdx.x == 32 && blockIdx.x + SMS < gridDim.x) {
+        // one CTA per SM has nobody to hide its loads behind: what the CTA a wave later reads is brought into L2, now that
+        // this wave's loads are done
+        const int u2 = (int)((blockIdx.x + SMS) / a.H), h2 = (int)((blockIdx.x + SMS) % a.H);
+        LinPiece p2;
+        if (lin_piece(a, u2, C, p2) && p2.len > 0) {
+            const int tok2 = p2.t0 + p2.j * C;
+            for (int k = 0; k < KATOMS; ++k) {
+                prefetch_tile(&f.tq, k * 64, h2, tok2);
+                prefetch_tile(&f.tk, k * 64, h2, tok2);
+            }
+            for (int t = 0; t < tiles; ++t) {
+                prefetch_tile(&f.to, t * DVT, h2, tok2);
+                prefetch_tile(&f.tv, t * DVT, h2, tok2);
+                bulk_prefetch(f.s.S + tile_at(u2, a.H, h2, tiles, t), TILE_FLOATS * 4);
+                bulk_prefetch(f.s.R + tile_at(u2, a.H, h2, tiles, t), TILE_FLOATS * 4);
+            }
+        }
+    }
     // ---- P and dA (bf16) to shared memory; the rows' and columns' sums of Z
     const float since = decay_since(d, row), until = decay_until(d, row);
     {
-        float z = 0.f;
+        f32x2 z2 = pk2(0.f, 0.f);
+        const float fs = a.scale * since;
+        const f32x2 fs2 = pk2(fs, fs);
 #pragma unroll 1
         for (int p = 0; p < 32; p += 16) {
             const int c0 = cg * 32 + p;
@@ -204,27 +236,37 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             if (cg <= q4) {
                 float x[16], y[16];
                 tmem_ld16x2(T_SC + lanes + c0, T_DP + lanes + c0, x, y);
-                const bool diagonal = cg == q4;
+                if (cg == q4) {               // the diagonal's block: zero above it, whatever the products hold there
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float g = a.scale * (d.factored ? since * d.b[c0 + j] : decay_pair(d, row, c0 + j));
-                    if (diagonal && c0 + j > row) g = 0.f;
-                    const float s = g == 0.f ? 0.f : x[j] * g, t = g == 0.f ? 0.f : y[j] * g;   // above the diagonal whatever the product holds
-                    x[j] = s;
-                    y[j] = t;
+                    for (int j = 0; j < 16; ++j) {
+                        x[j] = p + j <= lane ? x[j] : 0.f;
+                        y[j] = p + j <= lane ? y[j] : 0.f;
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    pb[j] = round_bf16x2(pk2(x[2 * j], x[2 * j + 1]));
-                    ab[j] = round_bf16x2(pk2(y[2 * j], y[2 * j + 1]));
-                }
-                // Z = P dP: dP again, without the factor (a second read costs less than 16 registers)
-                float dp[16];
-                tmem_ld16(T_DP + lanes + c0, dp);
+                for (int j = 0; j < 16; j += 4) {
+                    f32x2 g[2];
+                    if (d.factored) {
+                        const float4 b = *reinterpret_cast<const float4 *>(d.b + c0 + j);
+                        g[0] = mul2(fs2, pk2(b.x, b.y));
+                        g[1] = mul2(fs2, pk2(b.z, b.w));
+                    } else {                  // (above the diagonal a factor may be infinite)
+                        float e[4];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    x[j] = x[j] == 0.f ? 0.f : x[j] * dp[j];
-                    z += x[j];
+                        for (int i = 0; i < 4; ++i) e[i] = c0 + j + i <= row ? a.scale * decay_pair(d, row, c0 + j + i) : 0.f;
+                        g[0] = pk2(e[0], e[1]);
+                        g[1] = pk2(e[2], e[3]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = j + 2 * i;
+                        const f32x2 v = pk2(y[k], y[k + 1]), pp = mul2(pk2(x[k], x[k + 1]), g[i]), zz = mul2(pp, v);
+                        pb[k / 2] = round_bf16x2(pp);
+                        ab[k / 2] = round_bf16x2(mul2(v, g[i]));
+                        z2 = add2(z2, zz);
+                        x[k] = x2(zz);
+                        x[k + 1] = y2(zz);
+                    }
                 }
                 const float s = sum16(x, lane);
                 if (!(lane & 1)) zc[q4 * C + c0 + (lane >> 1)] = s;
@@ -239,8 +281,11 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
                 *reinterpret_cast<uint4 *>(sm + L_::DA + tile + off) = make_uint4(ab[4 * j], ab[4 * j + 1], ab[4 * j + 2], ab[4 * j + 3]);
             }
         }
-        zr[cg * C + row] = z;
+        zr[cg * C + row] = x2(z2) + y2(z2);
     }
+    wait_tma();
+    zero_tail(L_::Q, KATOMS);
+    if (L < C) __syncthreads();               // (a row's channels are read by other threads than cleared them)
     // ---- the states' parts of dQ and dK: dot products with q and k, rows scaled in place
     if (cg < 2 * KATOMS) {
         const float fa = a.scale * since, fw = until;
@@ -278,7 +323,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     if (lane == 0) sr_w[warp] = sr;
     publish();
 
-    // ---- the rest of the products, for the resident (last) half of d_v
+    // ---- the rest of the products: dV's parts for the resident (last) half of d_v, dQ, dK
     const int last = (tiles - 1) & ~1;
     auto value_parts = [&]() {                // P^T dO into the scores' columns, K R into dP's
         if (nt == 2) {
@@ -288,12 +333,14 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             mma_tiles<8, true, true, 64>(T_SC, sb + L_::P, sb + L_::DO, false);
             mma_tiles<4 * KATOMS, false, true, 64>(T_DP, sb + L_::K, sb + L_::R1, false);
         }
+        mma_commit(bar_a);
     };
     if (one) {
-        mma_tiles<8, false, true, NK>(T_DQ, sb + L_::DA, sb + L_::K, true);
-        mma_tiles<8, true, true, NK>(T_DK, sb + L_::DA, sb + L_::Q, true);
         value_parts();
-        mma_commit(bar_mma);
+        mma_tiles<8, false, true, NK>(T_DQ, sb + L_::DA, sb + L_::K, true);
+        mma_commit(bar_b);
+        mma_tiles<8, true, true, NK>(T_DK, sb + L_::DA, sb + L_::Q, true);
+        mma_commit(bar_c);                    // (a barrier of its own: it must not run a phase ahead of a waiter)
     }
     // meanwhile one warp sums up the decay's gradient, four tokens per lane
     if (f.b.dg && warp == 1) {
@@ -344,10 +391,9 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             if (lane == 0) f.s.share[(size_t)u * a.H + h] = sum;
         }
     }
-    wait_mma();
 
-    // ---- out: 32 columns of a warp's 32 rows at a time through shared memory that no MMA reads any more, so that four
-    // lanes share a row's 64 bytes in memory
+    // ---- out, each as its products are done: 32 columns of a warp's 32 rows at a time through shared memory that no MMA
+    // reads any more, so that four lanes share a row's 64 bytes in memory
     auto put = [&](bf16 *dst, int width, int col, int tile, const float (&x)[32]) {
         if (col >= width) return;
         const int base = tile + (col >> 6) % 2 * ATOM;
@@ -377,18 +423,28 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             put(static_cast<bf16 *>(f.b.dv), a.dv, t0 * DVT + cg * 32, L_::DO, x);
         }
     };
+    wait_a();
+    put_values(last);
+    wait_b();
     if (cg < 2 * KATOMS) {
         float x[32];
         tmem_ld32(T_DQ + lanes + cg * 32, x);
-        put(static_cast<bf16 *>(f.b.dq), a.dk, cg * 32, tiles > 2 ? L_::DA : L_::Q, x);   // K and P are read once more for the first half
-        tmem_ld32(T_DK + lanes + cg * 32, x);
-        put(static_cast<bf16 *>(f.b.dk), a.dk, cg * 32, tiles > 2 ? L_::DA : L_::Q, x);
+        put(static_cast<bf16 *>(f.b.dq), a.dk, cg * 32, L_::R1, x);
     }
-    put_values(last);
+    w.wait(bar_c, 0);
+    tc_fence_after();
+    if (cg < 2 * KATOMS) {
+        float x[32];
+        tmem_ld32(T_DK + lanes + cg * 32, x);
+        put(static_cast<bf16 *>(f.b.dk), a.dk, cg * 32, L_::DA, x);
+    }
     // ---- the first half's dV (d_v = 256)
     for (int t0 = last - 2; t0 >= 0; t0 -= 2) {
         publish();                            // the tiles that were written through are read, TMEM too
-        load_half(t0, false);
+        if (threadIdx.x == 0) {
+            mbar_expect_tx(bar_tma, (uint32_t)nt * ATOM);
+            load(&f.to, L_::DO, t0 * DVT, nt);
+        }
         for (int t = 0; t < nt; ++t) {
             fetch(f.s.R, t0 + t, R);
 #pragma unroll
@@ -401,11 +457,8 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
         wait_tma();
         zero_tail(L_::DO, nt);
         publish();
-        if (one) {
-            value_parts();
-            mma_commit(bar_mma);
-        }
-        wait_mma();
+        if (one) value_parts();
+        wait_a();
         put_values(t0);
     }
 
@@ -418,10 +471,10 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             drain(bar_tma, 1);
         }
         if (one) {
-            mbar_init(bar_mma, 1);
+            mbar_init(bar_a, 1);
             mbar_fence_init();
-            mma_commit(bar_mma);
-            drain(bar_mma, 0);
+            mma_commit(bar_a);
+            drain(bar_a, 0);
         }
         __syncthreads();
     }

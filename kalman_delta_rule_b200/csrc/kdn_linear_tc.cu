@@ -122,11 +122,6 @@ __device__ __forceinline__ void add_delta(f32x2 (&S)[16], uint32_t d, float2 dec
     }
 }
 
-__device__ __forceinline__ void prefetch_tile(const CUtensorMap *m, int c0, int h, int tok) {
-    tma_prefetch_3d(m, c0, h, tok);
-    tma_prefetch_3d(m, c0, h, tok + 64);
-}
-
 }  // namespace
 
 // ================================================================= decay records

@@ -162,6 +162,11 @@ __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, in
     tma_load_3d(dst, m, c0, h, tok, bar);
     tma_load_3d(dst + ATOM / 2, m, c0, h, tok + 64, bar);
 }
+// the same tile brought into L2
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap *m, int c0, int h, int tok) {
+    tma_prefetch_3d(m, c0, h, tok);
+    tma_prefetch_3d(m, c0, h, tok + 64);
+}
 // after a wait gave up: one more bounded wait for a barrier that copies or MMAs in flight still arrive on
 static __device__ __noinline__ void drain(uint64_t *bar, uint32_t parity) { mbar_wait(bar, parity, 100000000ll); }
 
