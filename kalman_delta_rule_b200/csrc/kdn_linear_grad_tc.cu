@@ -11,8 +11,6 @@
 // two parts of dV.  Rounding: P and dA, and R in K R, are bf16 (dq, dk and dv are); S and R enter the
 // products that dg is summed from as three bf16 terms, so dg keeps fp32's accuracy.
 // Per chunk and head at d = 128: 12 products of 128 x 128 x 128 (6100 cycles of MMA), 352 KB in and 96 KB out.
-#include <type_traits>
-
 #include "kdn_launch.h"
 #include "kdn_linear_tc.cuh"
 
@@ -65,10 +63,10 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     const LinArgs &a = f.b.a;
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H;
     LinPiece pc;
-    if (!lin_piece(a, u, C, pc) || pc.len == 0) return;
+    if (!uniform(lin_piece(a, u, C, pc) && pc.len > 0)) return;
     const int tok = pc.t0 + pc.j * C, L = min(C, pc.len - pc.j * C);
     const int tiles = (a.dv + DVT - 1) / DVT, nt = min(tiles, 2);        // tiles of d_v, of a half that is resident
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp & 3, cg = warp >> 2;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, q4 = warp & 3, cg = warp >> 2;
     const int row = q4 * 32 + lane;
     const uint32_t lanes = ((uint32_t)q4 * 32u) << 16;
 
@@ -93,7 +91,6 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t T_SC = tmem, T_DP = tmem + 128, T_DQ = tmem + 256, T_DK = tmem + 384;
-    const bool one = warp == 0 && elect_one();
     // every thread takes every wait and every barrier; after a wait that gave up the rest give up at once
     uint32_t ph_tma = 0, ph_a = 0, ph_b = 0;  // MMAs are committed to two barriers in turn
     auto wait_tma = [&]() { w.wait(bar_tma, ph_tma); ph_tma ^= 1; };
@@ -114,7 +111,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = __ldg(reinterpret_cast<const float4 *>(tile + ((cg * 4 + j) * 128 + row) * 4));
     };
-    auto terms = [&](const float4 (&x)[4], auto rounded, int p0, int p1, int p2) {
+    auto terms = [&](const float4 (&x)[4], int p0, int p1, int p2) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint32_t o[3][4];
@@ -122,7 +119,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             for (int i = 0; i < 4; ++i) {
                 const float4 y = x[2 * j + (i >> 1)];
                 uint32_t t[3];
-                split3<decltype(rounded)::value>(i & 1 ? pk2(y.z, y.w) : pk2(y.x, y.y), t);
+                split3(i & 1 ? pk2(y.z, y.w) : pk2(y.x, y.y), t);
                 o[0][i] = t[0]; o[1][i] = t[1]; o[2][i] = t[2];
             }
             const uint32_t off = swz(row, (cg * 2 + j) * 16);
@@ -171,9 +168,9 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             zero_tail(L_::DO, nt);
         }
         if (t > 0) wait_a();
-        terms(S, std::false_type(), L_::ST, L_::ST + ATOM, L_::ST + 2 * ATOM);
+        terms(S, L_::ST, L_::ST + ATOM, L_::ST + 2 * ATOM);
         publish();
-        if (one) {
+        if (warp == 0 && elect_one()) {
             if (t == 0) {
                 mma_tiles<4 * KATOMS, false, false, 128>(T_SC, sb + L_::Q, sb + L_::K, false);
                 mma_commit(bar_b);
@@ -187,9 +184,9 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
         for (int j = 0; j < 4; ++j) sr += S[j].x * R[j].x + S[j].y * R[j].y + S[j].z * R[j].z + S[j].w * R[j].w;
         if (t + 1 < tiles) fetch(f.s.S, t + 1, S);
         if (i == 1 || t == 0) wait_b();       // the scores (q's place is free), or the products of R's terms before
-        terms(R, std::true_type(), L_::R1 + i * ATOM, L_::R2, L_::R2 + ATOM);
+        terms(R, L_::R1 + i * ATOM, L_::R2, L_::R2 + ATOM);
         publish();
-        if (one) {
+        if (warp == 0 && elect_one()) {
             mma_tiles<4, false, false, NK>(T_DK, sb + L_::V + i * ATOM, sb + L_::R1 + i * ATOM, t > 0);
 #pragma unroll 1
             for (int p = 0; p < 2; ++p) mma_tiles<4, false, false, NK>(T_DK, sb + L_::V + i * ATOM, sb + L_::R2 + p * ATOM, true);
@@ -335,7 +332,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
         }
         mma_commit(bar_a);
     };
-    if (one) {
+    if (warp == 0 && elect_one()) {
         value_parts();
         mma_tiles<8, false, true, NK>(T_DQ, sb + L_::DA, sb + L_::K, true);
         mma_commit(bar_b);
@@ -345,12 +342,15 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     // meanwhile one warp sums up the decay's gradient, four tokens per lane
     if (f.b.dg && warp == 1) {
         float s0 = 0.f;
+#pragma unroll 1
         for (int i = 0; i < NT / 32; ++i) s0 += sr_w[i];
         const float whole = d.whole.x * s0;
         Log2 later[4], earlier[4];            // sums in two floats, as for the decays
+#pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int t = lane * 4 + e;
             float rows = 0.f, cols = 0.f, x = 0.f, y = 0.f;
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 rows += zr[i * C + t];
                 cols += zc[i * C + t];
@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
         }
         Log2 sl = (later[0] + later[1]) + (later[2] + later[3]), se = (earlier[0] + earlier[1]) + (earlier[2] + earlier[3]);
         Log2 fl = sl, fe = se;
+#pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
             const Log2 yl = {__shfl_down_sync(0xffffffffu, fl.hi, off), __shfl_down_sync(0xffffffffu, fl.lo, off)};
             const Log2 ye = {__shfl_up_sync(0xffffffffu, fe.hi, off), __shfl_up_sync(0xffffffffu, fe.lo, off)};
@@ -393,50 +394,47 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     }
 
     // ---- out, each as its products are done: 32 columns of a warp's 32 rows at a time through shared memory that no MMA
-    // reads any more, so that four lanes share a row's 64 bytes in memory
-    auto put = [&](bf16 *dst, int width, int col, int tile, const float (&x)[32]) {
-        if (col >= width) return;
-        const int base = tile + (col >> 6) % 2 * ATOM;
+    // reads any more, so that four lanes share a row's 64 bytes in memory.  which: 0 dv, 1 dq, 2 dk (one piece of code:
+    // a CTA passes here once, and what it executes has to be fetched)
+    auto put = [&](int which, int t0) {
+        const int width = which ? a.dk : a.dv, col = t0 * DVT + cg * 32, in = cg * 32;
+        if (col >= width || in >= (which ? NK : nt * DVT)) return;
+        uint8_t *tile = sm + (which == 0 ? L_::DO : which == 1 ? L_::R1 : L_::DA) + (in >> 6) * ATOM;
+        const uint32_t acc = (which == 0 ? T_SC : which == 1 ? T_DQ : T_DK) + lanes + in;
+        bf16 *dst = static_cast<bf16 *>(which == 0 ? f.b.dv : which == 1 ? f.b.dq : f.b.dk);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t z[4];
+        for (int p = 0; p < 32; p += 16) {
+            float x[16], y[16];
+            tmem_ld16x2(acc + p, T_DP + lanes + in + p, x, y);
+            const f32x2 f2 = pk2(until, until);
+            uint32_t z[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = round_bf16x2(pk2(x[8 * j + 2 * i], x[8 * j + 2 * i + 1]));
-            *reinterpret_cast<uint4 *>(sm + base + swz(row, (col & 63) * 2 + j * 16)) = make_uint4(z[0], z[1], z[2], z[3]);
+            for (int j = 0; j < 8; ++j) {
+                f32x2 v = pk2(x[2 * j], x[2 * j + 1]);
+                if (which == 0) v = fma2(f2, pk2(y[2 * j], y[2 * j + 1]), v);
+                z[j] = round_bf16x2(v);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<uint4 *>(tile + swz(row, (in & 63) * 2 + p * 2 + j * 16)) = make_uint4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
         }
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < 32; r += 8) {
             const int t = q4 * 32 + r + (lane >> 2);
-            const uint4 z = *reinterpret_cast<const uint4 *>(sm + base + swz(t, (col & 63) * 2 + (lane & 3) * 16));
+            const uint4 z = *reinterpret_cast<const uint4 *>(tile + swz(t, (in & 63) * 2 + (lane & 3) * 16));
             if (t < L) *reinterpret_cast<uint4 *>(dst + ((size_t)(tok + t) * a.H + h) * width + col + (lane & 3) * 8) = z;
         }
-        __syncwarp();
     };
-    auto put_values = [&](int t0) {
-        if (cg < 2 * nt) {
-            float x[32], y[32];
-            tmem_ld32(T_SC + lanes + cg * 32, x);
-            tmem_ld32(T_DP + lanes + cg * 32, y);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = fmaf(until, y[j], x[j]);
-            put(static_cast<bf16 *>(f.b.dv), a.dv, t0 * DVT + cg * 32, L_::DO, x);
+#pragma unroll 1
+    for (int which = 0; which < 3; ++which) {
+        if (which == 0) wait_a();
+        if (which == 1) wait_b();
+        if (which == 2) {
+            w.wait(bar_c, 0);
+            tc_fence_after();
         }
-    };
-    wait_a();
-    put_values(last);
-    wait_b();
-    if (cg < 2 * KATOMS) {
-        float x[32];
-        tmem_ld32(T_DQ + lanes + cg * 32, x);
-        put(static_cast<bf16 *>(f.b.dq), a.dk, cg * 32, L_::R1, x);
-    }
-    w.wait(bar_c, 0);
-    tc_fence_after();
-    if (cg < 2 * KATOMS) {
-        float x[32];
-        tmem_ld32(T_DK + lanes + cg * 32, x);
-        put(static_cast<bf16 *>(f.b.dk), a.dk, cg * 32, L_::DA, x);
+        put(which, which == 0 ? last : 0);
     }
     // ---- the first half's dV (d_v = 256)
     for (int t0 = last - 2; t0 >= 0; t0 -= 2) {
@@ -457,9 +455,9 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
         wait_tma();
         zero_tail(L_::DO, nt);
         publish();
-        if (one) value_parts();
+        if (warp == 0 && elect_one()) value_parts();
         wait_a();
-        put_values(t0);
+        put(0, t0);
     }
 
     tc_fence_before();
@@ -470,7 +468,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             drain(bar_tma, 0);
             drain(bar_tma, 1);
         }
-        if (one) {
+        if (warp == 0 && elect_one()) {
             mbar_init(bar_a, 1);
             mbar_fence_init();
             mma_commit(bar_a);

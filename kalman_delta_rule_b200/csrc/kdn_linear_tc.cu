@@ -189,12 +189,12 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
     const LinArgs &a = f.a;
     const int tiles = (a.dv + DVT - 1) / DVT;
     const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % a.H, u = blockIdx.x / tiles / a.H;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     constexpr int W_S = NW_W, W_MMA = W_S + NW_S, W_TMA = W_MMA + 1;   // MMA beside the rows with the fewest scores
     LinPiece pc;
-    if (!lin_piece(a, u, f.sp.seg, pc)) return;
+    if (!uniform(lin_piece(a, u, f.sp.seg, pc))) return;
     const int tok0 = pc.t0 + pc.j * f.sp.seg, len = min(f.sp.seg, pc.len - pc.j * f.sp.seg);
-    const int n = (len + C - 1) / C;
+    const int n = uniform((len + C - 1) / C);
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L_::BAR);
     uint64_t *qk_full = bar, *v_full = bar + 2, *q_free = bar + 4, *k_free = bar + 6, *v_free = bar + 8, *dec_full = bar + 10,
@@ -410,33 +410,32 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
         }
     } else if (warp == W_MMA) {
         // ---------------------------------------------------------- MMA (the warp waits, one lane issues)
-        const bool one = elect_one();
         for (int c = 0; c < n; ++c) {
-            const int st = __shfl_sync(0xffffffffu, c & 1, 0);   // (uniform to the compiler: descriptors stay in uniform registers)
-            if (!w.wait(qk_full + st, (c >> 1) & 1)) break;
+            const int st = c & 1;
+            if (!w.wait_all(qk_full + st, (c >> 1) & 1)) break;
             tc_fence_after();
-            if (one) {                        // (the scores before were read before P V of the chunk before)
+            if (elect_one()) {                        // (the scores before were read before P V of the chunk before)
                 mma_tiles<4 * KATOMS, false, false, 128>(T_SC, sb + L_::Q + st * 2 * ATOM, sb + L_::K + st * 2 * ATOM, false);
                 mma_commit(sc_full);
             }
-            if (!w.wait(vp_full, c & 1) || (c > 0 && !w.wait(dl_free, (c - 1) & 1))) break;
+            if (!w.wait_all(vp_full, c & 1) || (c > 0 && !w.wait_all(dl_free, (c - 1) & 1))) break;
             tc_fence_after();
-            if (one) {
+            if (elect_one()) {
                 mma_delta(T_DL, sb + L_::K + st * 2 * ATOM, sb + L_::VP);
                 mma_commit(dl_full);
                 mma_commit(k_free + st);
             }
-            if (!w.wait(s_full, c & 1) || (c > 0 && !w.wait(o_free, (c - 1) & 1))) break;
+            if (!w.wait_all(s_full, c & 1) || (c > 0 && !w.wait_all(o_free, (c - 1) & 1))) break;
             tc_fence_after();
-            if (one) {
+            if (elect_one()) {
                 mma_tiles<4 * KATOMS, false, true, 64>(T_OS, sb + L_::Q + st * 2 * ATOM, sb + L_::S, false);
                 mma_commit(q_free + st);
             }
-            if (!w.wait(p_full, c & 1)) break;
+            if (!w.wait_all(p_full, c & 1)) break;
             tc_fence_after();
-            if (one) {
+            if (elect_one()) {
                 const uint64_t dv = tile_mnmajor(sb + L_::V + st * ATOM);
-#pragma unroll
+#pragma unroll 4
                 for (int ks = 0; ks < 8; ++ks)
                     mma_bf16_ta(T_OI, T_P + ks * 8, dv + step_mnmajor(ks), idesc_bf16(128, 64, false, true), ks > 0);
                 mma_commit(o_full);
@@ -487,17 +486,17 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
     const LinArgs &a = f.a;
     const int tiles = (a.dv + DVT - 1) / DVT;
     const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % a.H, u = blockIdx.x / tiles / a.H;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     constexpr int W_MMA = NW_W + NW_S, W_TMA = W_MMA + 1;
     LinPiece pc;
-    if (!lin_piece(a, u, f.piece, pc)) return;
+    if (!uniform(lin_piece(a, u, f.piece, pc))) return;
     const int per = f.sp.seg / f.sp.sub;
     if (TOTALS) {
         const int seg = pc.j / per, last = pc.len > 0 ? (pc.len - 1) / f.sp.seg : 0;
-        if (REV ? seg == 0 : seg == last) return;
+        if (uniform(REV ? seg == 0 : seg == last)) return;
     }
     const int tok0 = pc.t0 + pc.j * f.piece, len = min(f.piece, pc.len - pc.j * f.piece);
-    const int n = (len + C - 1) / C;
+    const int n = uniform((len + C - 1) / C);
     auto chunk = [&](int c) { return REV ? n - 1 - c : c; };
     const int c0 = lin_first_slot(a, pc.s, pc.t0, C) + pc.j * (f.piece / C);   // the piece's first chunk's slot
 
@@ -623,13 +622,12 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
             }
         }
     } else if (warp == W_MMA) {
-        const bool one = elect_one();
         for (int c = 0; c < n; ++c) {
-            const int st = __shfl_sync(0xffffffffu, c & 1, 0);
-            if (!w.wait(x_full + st, (c >> 1) & 1) || !w.wait(vp_full + st, (c >> 1) & 1)) break;
-            if (c >= 2 && !w.wait(dl_free + st, ((c >> 1) - 1) & 1)) break;
+            const int st = c & 1;
+            if (!w.wait_all(x_full + st, (c >> 1) & 1) || !w.wait_all(vp_full + st, (c >> 1) & 1)) break;
+            if (c >= 2 && !w.wait_all(dl_free + st, ((c >> 1) - 1) & 1)) break;
             tc_fence_after();
-            if (one) {
+            if (elect_one()) {
                 mma_delta(tmem + st * 192, sb + L_::X + st * 2 * ATOM, sb + L_::VP + st * 3 * ATOM);
                 mma_commit(dl_full + st);
                 mma_commit(x_free + st);

@@ -37,7 +37,13 @@ struct Waits {
     __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
         return mbar_try_wait_for(bar, parity, 1000000u) || wait_slowly(bar, parity, abort_flag);
     }
+    // one answer for the warp
+    __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity) const { return __all_sync(0xffffffffu, wait(bar, parity)); }
 };
+// A value that is the same in every lane, in a form that shows it to the compiler: around the MMAs every
+// branch and loop has to be provably one for the warp, or each of their operands is moved to uniform registers
+// lane by lane (see elect_one)
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 // all lanes' writes before this are behind the arrival of the warp's one lane
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
@@ -72,33 +78,19 @@ __device__ __forceinline__ float decay_pair(const Decay &d, int t, int s) {   //
 }
 
 // ------------------------------------------------------------------ three bf16 terms of an fp32 value
-// x = t0 + t1 + t2 exactly (barring underflow): each term takes the leading 8 of the 24 bits that are left, by
-// truncation.  So the products that fp32 states are summed from keep fp32's accuracy through bf16 operands
-// (two terms would leave 2^-16).  No conversion instruction: cvt.rn.bf16x2 runs at about 8 lanes per clock and
-// SM, which bounded the whole kernel when every packing used it (XU pipe 89% busy).
 __device__ __forceinline__ f32x2 unpack2(uint32_t u) { return pk2(bf16_lo(u), bf16_hi(u)); }
-__device__ __forceinline__ uint32_t upper_halves(f32x2 x) {   // two bf16 by truncation
-    return __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
-}
-__device__ __forceinline__ f32x2 trunc2(f32x2 x) { return x & 0xffff0000ffff0000ull; }
-// two fp32 rounded to nearest bf16 on the FMA pipe: with c = (2^16 + 1) x, c - (c - x) has the leading 8
-// bits (Veltkamp's splitting; beyond 2^111 the result is not a number, as for an infinity).  c is a rounded fma:
-// a packed product may be contracted with the subtraction, which would undo the rounding it is there for.
-__device__ __forceinline__ uint32_t round_bf16x2(f32x2 x) {
-    const f32x2 c = fma2(x, pk2(65536.f, 65536.f), x);
-    return upper_halves(sub2(c, sub2(c, x)));
+__device__ __forceinline__ uint32_t round_bf16x2(f32x2 x) { return pack_bf16x2(x2(x), y2(x)); }
+// x = t0 + t1 + t2 exactly (barring underflow): each term is the nearest bf16 to what is left of the 24 bits.  So
+// the products that fp32 states are summed from keep fp32's accuracy through bf16 operands (two terms would
+// leave 2^-17); the first term alone is x rounded to bf16.
+__device__ __forceinline__ void split3(f32x2 x, uint32_t (&t)[3]) {
+    t[0] = round_bf16x2(x);
+    x = sub2(x, unpack2(t[0]));
+    t[1] = round_bf16x2(x);
+    x = sub2(x, unpack2(t[1]));
+    t[2] = round_bf16x2(x);
 }
 
-// ROUND: the first term rounded to nearest (the rest may then be negative; it still has 16 bits), for terms of
-// which the first serves alone somewhere
-template <bool ROUND = false>
-__device__ __forceinline__ void split3(f32x2 x, uint32_t (&t)[3]) {
-    t[0] = ROUND ? round_bf16x2(x) : upper_halves(x);
-    x = sub2(x, ROUND ? unpack2(t[0]) : trunc2(x));
-    t[1] = upper_halves(x);
-    x = sub2(x, trunc2(x));
-    t[2] = upper_halves(x);
-}
 // half a row of a [128][64] bf16 tile, weighted, as three terms in three tiles (thread = row x half)
 __device__ __forceinline__ void weigh_row(const uint8_t *src, uint8_t *dst, int row, int half, float w) {
 #pragma unroll 2
@@ -131,21 +123,17 @@ __device__ __forceinline__ uint64_t tile_mnmajor(uint32_t tile) { return sdesc(t
 __host__ __device__ constexpr uint32_t step_kmajor(int ks) { return ((ks >> 2) * ATOM + (ks & 3) * 32) >> 4; }
 __host__ __device__ constexpr uint32_t step_mnmajor(int ks) { return ks * 2048 >> 4; }
 
-// D (+)= A B over STEPS K steps (a multiple of 4), both operands in shared memory
+// D (+)= A B over STEPS K steps, both operands in shared memory.  Unrolled: with the tile's address uniform over the
+// warp the descriptors are uniform registers plus constants, and a step costs the issuing thread some 20 cycles
 template <int STEPS, bool A_MN, bool B_MN, int N>
 __device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a, uint32_t b, bool acc) {
     constexpr uint32_t ID = idesc_bf16(128, N, A_MN, B_MN);
-    uint64_t da = A_MN ? tile_mnmajor(a) : tile_kmajor(a), db = B_MN ? tile_mnmajor(b) : tile_kmajor(b);
-#pragma unroll 1
-    for (int k4 = 0; k4 < STEPS / 4; ++k4) {
+    const uint64_t da = A_MN ? tile_mnmajor(a) : tile_kmajor(a), db = B_MN ? tile_mnmajor(b) : tile_kmajor(b);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-            mma_bf16(d, da + (A_MN ? step_mnmajor(ks) : step_kmajor(ks)), db + (B_MN ? step_mnmajor(ks) : step_kmajor(ks)), ID, acc || ks > 0);
-        da += A_MN ? step_mnmajor(4) : step_kmajor(4);
-        db += B_MN ? step_mnmajor(4) : step_kmajor(4);
-        acc = true;
-    }
+    for (int ks = 0; ks < STEPS; ++ks)
+        mma_bf16(d, da + (A_MN ? step_mnmajor(ks) : step_kmajor(ks)), db + (B_MN ? step_mnmajor(ks) : step_kmajor(ks)), ID, acc || ks > 0);
 }
+
 // delta[dk, dv tile] = X^T [Y0 Y1 Y2]: 64 columns for each term, so that X is read from shared memory once
 __device__ __forceinline__ void mma_delta(uint32_t d, uint32_t x, uint32_t y) { mma_tiles<8, true, true, 192>(d, x, y, false); }
 
