@@ -9,7 +9,8 @@
 //   TMA      refills Q, K, the V tile and the decay record for chunk c + 2, each as soon as chunk c is done with it
 //   MMA      one thread: scores = Q K^T, delta = K^T V', OS = Q S, OI = P V (P from TMEM)
 //   W (8)    V' = diag(e^{G_C - G}) V as three bf16 terms; scores (TMEM) -> decayed, masked, bf16 -> P (TMEM)
-//   S (8)    S <- e^{G_C} S + delta in registers (fp32), its bf16 copy for Q S; o = scale (OI + e^G OS)
+//   S (8)    S <- e^{G_C} S + delta in registers (fp32), its bf16 copy for Q S
+//   O (4)    o = scale (OI + e^G OS)
 // What bounds it is one pass over q, k, v and o at HBM's rate; the MMAs take about 2050 cycles per chunk
 // and tile (scores 512, Q S 384, delta 896 -- its A operand is read from shared memory three times --,
 // P V 256), which is about what the chunk's bytes take at an SM's share of the bandwidth.
@@ -30,9 +31,9 @@ using namespace lin;
 
 namespace {
 
-// warps: W weighted rows (forward: and scores), S state (forward: and outputs); then MMA and TMA
-constexpr int NW_W = 8, NW_S = 8;
-constexpr int NT_F = (NW_W + NW_S + 2) * 32;
+// warps: W weighted rows (forward: and scores), S state, O outputs (forward); then MMA and TMA
+constexpr int NW_W = 8, NW_S = 8, NW_O = 4;
+constexpr int NT_F = (NW_W + NW_S + NW_O + 2) * 32;
 constexpr int NT_S = (NW_W + NW_S + 2) * 32;
 
 struct FwdSmem {
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
     const int tiles = (a.dv + DVT - 1) / DVT;
     const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % a.H, u = blockIdx.x / tiles / a.H;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    constexpr int W_S = NW_W, W_MMA = W_S + NW_S, W_TMA = W_MMA + 1;   // MMA beside the rows with the fewest scores
+    constexpr int W_S = NW_W, W_O = W_S + NW_S, W_MMA = W_O + NW_O, W_TMA = W_MMA + 1;   // MMA beside the rows with the fewest scores
     LinPiece pc;
     if (!uniform(lin_piece(a, u, f.sp.seg, pc))) return;
     const int tok0 = pc.t0 + pc.j * f.sp.seg, len = min(f.sp.seg, pc.len - pc.j * f.sp.seg);
@@ -211,14 +212,14 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
             mbar_init(v_full + i, 1);
             mbar_init(q_free + i, 1);
             mbar_init(k_free + i, 1);
-            mbar_init(v_free + i, NW_S);
+            mbar_init(v_free + i, NW_O);
             mbar_init(dec_full + i, 1);
-            mbar_init(dec_free + i, NW_W + NW_S);
+            mbar_init(dec_free + i, NW_W + NW_S + NW_O);
         }
         mbar_init(sc_full, 1);
         mbar_init(p_full, NW_W);
         mbar_init(o_full, 1);
-        mbar_init(o_free, NW_S);
+        mbar_init(o_free, NW_O);
         mbar_init(dl_full, 1);
         mbar_init(dl_free, NW_S);
         mbar_init(vp_full, NW_W);
@@ -300,8 +301,8 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
             warp_arrive(p_full);
             warp_arrive(dec_free + st);
         }
-    } else if (warp < W_MMA) {
-        // ---------------------------------------------------------- S: the state, then the outputs
+    } else if (warp < W_O) {
+        // ---------------------------------------------------------- S: the state
         const int half = (warp - W_S) >> 2;
         const int col = tile * DVT + half * 32;
         const size_t se = ((size_t)pc.s * a.H + h) * a.dk * a.dv;
@@ -310,74 +311,76 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
         const int before = pc.j * (f.sp.seg / f.sp.sub), s0 = lin_first_slot(a, pc.s, pc.t0, f.sp.sub);
         for (int i = 0; i < before; ++i)
             fold_tile(S, f.sp.U + tile_at(s0 + i, a.H, h, tiles, tile), f.sp.dec[(size_t)(s0 + i) * a.H + h], row, half);
-        // the outputs go through the chunk's V tile, which its MMAs are done with: a warp's 32 rows x 64 bytes there
-        // and back, so that four lanes share a row's 64 bytes in memory (a row per lane costs 4 times the LSU cycles)
-        bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(tok0 + (warp & 3) * 32 + (lane >> 2)) * a.H + h) * a.dv + col + (lane & 3) * 8;
-        float fs = 0.f, fi = 0.f;
         bool ok = true;
-        for (int c = 0; c <= n; ++c) {
+        for (int c = 0; c < n; ++c) {
+            const int st = c & 1;
             // the bf16 copy that chunk c's Q S reads, once the Q S before has
-            if (c > 0) ok = w.wait(q_free + ((c - 1) & 1), ((c - 1) >> 1) & 1);
+            if (c > 0) ok = w.wait(q_free + (st ^ 1), ((c - 1) >> 1) & 1);
             if (!ok) break;
-            if (c < n) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t z[4];
+            for (int j = 0; j < 4; ++j) {
+                uint32_t z[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[i] = round_bf16x2(S[j * 4 + i]);
-                    *reinterpret_cast<uint4 *>(sm + L_::S + swz(row, (half * 4 + j) * 16)) = make_uint4(z[0], z[1], z[2], z[3]);
-                }
-                fence_async_smem();
-                warp_arrive(s_full);
+                for (int i = 0; i < 4; ++i) z[i] = round_bf16x2(S[j * 4 + i]);
+                *reinterpret_cast<uint4 *>(sm + L_::S + swz(row, (half * 4 + j) * 16)) = make_uint4(z[0], z[1], z[2], z[3]);
             }
-            if (c > 0) {                      // o of the chunk before
-                const int st = (c - 1) & 1, L = min(C, len - (c - 1) * C);
-                const f32x2 fs2 = pk2(fs, fs), fi2 = pk2(fi, fi);
-                ok = w.wait(o_full, (c - 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int p = 0; p < 32; p += 16) {
-                    float x[16], y[16];
-                    tmem_ld16x2(T_OI + lanes + half * 32 + p, T_OS + lanes + half * 32 + p, x, y);
-                    if (p == 16) {
-                        tc_fence_before();
-                        warp_arrive(o_free);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        uint32_t z[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            z[i] = round_bf16x2(fma2(fi2, pk2(x[j + 2 * i], x[j + 2 * i + 1]), mul2(fs2, pk2(y[j + 2 * i], y[j + 2 * i + 1]))));
-                        *reinterpret_cast<uint4 *>(sm + L_::V + st * ATOM + swz(row, half * 64 + (p + j) * 2)) = make_uint4(z[0], z[1], z[2], z[3]);
-                    }
-                }
-                __syncwarp();
-#pragma unroll
-                for (int r = 0; r < 32; r += 8) {
-                    const int t = (warp & 3) * 32 + r + (lane >> 2);
-                    const uint4 z = *reinterpret_cast<const uint4 *>(sm + L_::V + st * ATOM + swz(t, half * 64 + (lane & 3) * 16));
-                    if (t < L && col < a.dv) *reinterpret_cast<uint4 *>(o + (size_t)r * a.H * a.dv) = z;
-                }
-                fence_async_smem();
-                warp_arrive(v_free + st);
-                o += (size_t)C * a.H * a.dv;
-            }
-            if (c < n) {
-                ok = w.wait(dec_full + (c & 1), (c >> 1) & 1) && w.wait(dl_full, c & 1);
-                if (!ok) break;
-                tc_fence_after();
-                add_delta(S, T_DL + lanes + half * 32, dec[c & 1].whole);
-                tc_fence_before();
-                warp_arrive(dl_free);
-                // factored: the row's 2^{G_t} is common to both parts of o (P holds the columns' 2^{-G_s})
-                fs = a.scale * decay_since(dec[c & 1], row);
-                fi = dec[c & 1].factored ? fs : a.scale;
-                warp_arrive(dec_free + (c & 1));
-            }
+            fence_async_smem();
+            warp_arrive(s_full);
+            ok = w.wait(dec_full + st, (c >> 1) & 1);
+            if (!ok) break;
+            const float2 whole = dec[st].whole;
+            warp_arrive(dec_free + st);
+            ok = w.wait(dl_full, c & 1);
+            if (!ok) break;
+            tc_fence_after();
+            add_delta(S, T_DL + lanes + half * 32, whole);
+            tc_fence_before();
+            warp_arrive(dl_free);
         }
         if (ok && a.S_out && (long long)(pc.j + 1) * f.sp.seg >= pc.len) store_caller(S, a.S_out + se, a.dk, a.dv, row, col);
+    } else if (warp < W_MMA) {
+        // ---------------------------------------------------------- O: the outputs, through the chunk's V tile, which its MMAs
+        // are done with: a warp's 32 rows x 128 bytes there and back, so that eight lanes share a row's 128 bytes in memory
+        // (a row per lane costs 8 times the LSU cycles, and the fences of the other roles wait behind them)
+        const int col = tile * DVT + (lane & 7) * 8;
+        bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(tok0 + (warp & 3) * 32 + (lane >> 3)) * a.H + h) * a.dv + col;
+        for (int c = 0; c < n; ++c) {
+            const int st = c & 1, L = min(C, len - c * C);
+            if (!w.wait(dec_full + st, (c >> 1) & 1)) break;
+            // factored: the row's 2^{G_t} is common to both parts of o (P holds the columns' 2^{-G_s})
+            const float fs = a.scale * decay_since(dec[st], row), fi = dec[st].factored ? fs : a.scale;
+            warp_arrive(dec_free + st);
+            const f32x2 fs2 = pk2(fs, fs), fi2 = pk2(fi, fi);
+            if (!w.wait(o_full, c & 1)) break;
+            tc_fence_after();
+#pragma unroll 2
+            for (int p = 0; p < 64; p += 16) {
+                float x[16], y[16];
+                tmem_ld16x2(T_OI + lanes + p, T_OS + lanes + p, x, y);
+                if (p == 48) {
+                    tc_fence_before();
+                    warp_arrive(o_free);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; j += 8) {
+                    uint32_t z[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        z[i] = round_bf16x2(fma2(fi2, pk2(x[j + 2 * i], x[j + 2 * i + 1]), mul2(fs2, pk2(y[j + 2 * i], y[j + 2 * i + 1]))));
+                    *reinterpret_cast<uint4 *>(sm + L_::V + st * ATOM + swz(row, (p + j) * 2)) = make_uint4(z[0], z[1], z[2], z[3]);
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < 32; r += 4) {
+                const int t = (warp & 3) * 32 + r + (lane >> 3);
+                const uint4 z = *reinterpret_cast<const uint4 *>(sm + L_::V + st * ATOM + swz(t, (lane & 7) * 16));
+                if (t < L && col < a.dv) *reinterpret_cast<uint4 *>(o + (size_t)r * a.H * a.dv) = z;
+            }
+            o += (size_t)C * a.H * a.dv;
+            fence_async_smem();
+            warp_arrive(v_free + st);
+        }
     } else if (warp == W_TMA) {
         // ---------------------------------------------------------- TMA: Q, K and V are refilled as each is free
         if (lane == 0) {
