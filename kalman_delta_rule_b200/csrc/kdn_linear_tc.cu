@@ -38,7 +38,7 @@ constexpr int NT_S = (NW_W + NW_S + 2) * 32;
 
 struct FwdSmem {
     static constexpr int Q = 0, K = Q + 2 * 2 * ATOM, V = K + 2 * 2 * ATOM, VP = V + 2 * ATOM, S = VP + 3 * ATOM,
-                         DEC = S + ATOM, BAR = DEC + 2 * (int)sizeof(Decay), NBAR = 22, CTL = BAR + NBAR * 8, TOTAL = CTL + 16;
+                         DEC = S + ATOM, BAR = DEC + 2 * (int)sizeof(Decay), NBAR = 20, CTL = BAR + NBAR * 8, TOTAL = CTL + 16;
 };
 static_assert(FwdSmem::TOTAL <= 227 * 1024, "shared memory");
 
@@ -199,8 +199,9 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L_::BAR);
     uint64_t *qk_full = bar, *v_full = bar + 2, *q_free = bar + 4, *k_free = bar + 6, *v_free = bar + 8, *dec_full = bar + 10,
-             *dec_free = bar + 12, *o_free = bar + 14, *sc_full = bar + 15, *p_full = bar + 16, *o_full = bar + 17,
-             *dl_full = bar + 18, *dl_free = bar + 19, *vp_full = bar + 20, *s_full = bar + 21;
+             *dec_free = bar + 12, *sc_full = bar + 14, *p_full = bar + 15, *o_full = bar + 16, *dl_full = bar + 17,
+             *delta_ok = bar + 18,             // the weighted rows are there, and the delta before has been read
+             *qs_ok = bar + 19;                // the state's copy is there, and the outputs before have been read
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L_::CTL);
     int *abort_flag = reinterpret_cast<int *>(sm + L_::CTL + 4);
     const Waits w{abort_flag};
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
             mbar_init(qk_full + i, 1);
             mbar_init(v_full + i, 1);
             mbar_init(q_free + i, 1);
-            mbar_init(k_free + i, 1);
+            mbar_init(k_free + i, NW_S);
             mbar_init(v_free + i, NW_O);
             mbar_init(dec_full + i, 1);
             mbar_init(dec_free + i, NW_W + NW_S + NW_O);
@@ -219,11 +220,9 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
         mbar_init(sc_full, 1);
         mbar_init(p_full, NW_W);
         mbar_init(o_full, 1);
-        mbar_init(o_free, NW_O);
         mbar_init(dl_full, 1);
-        mbar_init(dl_free, NW_S);
-        mbar_init(vp_full, NW_W);
-        mbar_init(s_full, NW_S);
+        mbar_init(delta_ok, NW_W + NW_S);
+        mbar_init(qs_ok, NW_S + NW_O);
         mbar_fence_init();
         *abort_flag = (sb & 1023u) ? 1 : 0;   // the swizzled tiles need 1 KB alignment
         tma_prefetch_desc(&f.tq);
@@ -266,7 +265,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
                 if (w.wait(qk_full + st, (c >> 1) & 1)) zero_row(sm + L_::K + (st * 2 + half) * ATOM, row, 0, 8);
             }
             fence_async_smem();
-            warp_arrive(vp_full);
+            warp_arrive(delta_ok);
 
             if (!w.wait(sc_full, c & 1)) break;
             tc_fence_after();
@@ -312,6 +311,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
         for (int i = 0; i < before; ++i)
             fold_tile(S, f.sp.U + tile_at(s0 + i, a.H, h, tiles, tile), f.sp.dec[(size_t)(s0 + i) * a.H + h], row, half);
         bool ok = true;
+        warp_arrive(delta_ok);                // (there is no delta before the first)
         for (int c = 0; c < n; ++c) {
             const int st = c & 1;
             // the bf16 copy that chunk c's Q S reads, once the Q S before has
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
                 *reinterpret_cast<uint4 *>(sm + L_::S + swz(row, (half * 4 + j) * 16)) = make_uint4(z[0], z[1], z[2], z[3]);
             }
             fence_async_smem();
-            warp_arrive(s_full);
+            warp_arrive(qs_ok);
             ok = w.wait(dec_full + st, (c >> 1) & 1);
             if (!ok) break;
             const float2 whole = dec[st].whole;
@@ -333,9 +333,10 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
             ok = w.wait(dl_full, c & 1);
             if (!ok) break;
             tc_fence_after();
+            warp_arrive(k_free + st);
             add_delta(S, T_DL + lanes + half * 32, whole);
             tc_fence_before();
-            warp_arrive(dl_free);
+            warp_arrive(delta_ok);
         }
         if (ok && a.S_out && (long long)(pc.j + 1) * f.sp.seg >= pc.len) store_caller(S, a.S_out + se, a.dk, a.dv, row, col);
     } else if (warp < W_MMA) {
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
         // (a row per lane costs 8 times the LSU cycles, and the fences of the other roles wait behind them)
         const int col = tile * DVT + (lane & 7) * 8;
         bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(tok0 + (warp & 3) * 32 + (lane >> 3)) * a.H + h) * a.dv + col;
+        warp_arrive(qs_ok);                   // (there are no outputs before the first)
         for (int c = 0; c < n; ++c) {
             const int st = c & 1, L = min(C, len - c * C);
             if (!w.wait(dec_full + st, (c >> 1) & 1)) break;
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
                 tmem_ld16x2(T_OI + lanes + p, T_OS + lanes + p, x, y);
                 if (p == 48) {
                     tc_fence_before();
-                    warp_arrive(o_free);
+                    warp_arrive(qs_ok);
                 }
 #pragma unroll
                 for (int j = 0; j < 16; j += 8) {
@@ -421,14 +423,13 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
                 mma_tiles<4 * KATOMS, false, false, 128>(T_SC, sb + L_::Q + st * 2 * ATOM, sb + L_::K + st * 2 * ATOM, false);
                 mma_commit(sc_full);
             }
-            if (!w.wait_all(vp_full, c & 1) || (c > 0 && !w.wait_all(dl_free, (c - 1) & 1))) break;
+            if (!w.wait_all(delta_ok, c & 1)) break;
             tc_fence_after();
             if (elect_one()) {
                 mma_delta(T_DL, sb + L_::K + st * 2 * ATOM, sb + L_::VP);
                 mma_commit(dl_full);
-                mma_commit(k_free + st);
             }
-            if (!w.wait_all(s_full, c & 1) || (c > 0 && !w.wait_all(o_free, (c - 1) & 1))) break;
+            if (!w.wait_all(qs_ok, c & 1)) break;
             tc_fence_after();
             if (elect_one()) {
                 mma_tiles<4 * KATOMS, false, true, 64>(T_OS, sb + L_::Q + st * 2 * ATOM, sb + L_::S, false);
@@ -461,10 +462,10 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
             }
         }
         if (warp == W_MMA && elect_one()) {
-            mbar_init(s_full, 1);
+            mbar_init(qs_ok, 1);
             mbar_fence_init();
-            mma_commit(s_full);
-            drain(s_full, 0);
+            mma_commit(qs_ok);
+            drain(qs_ok, 0);
         }
         __syncthreads();
     }
