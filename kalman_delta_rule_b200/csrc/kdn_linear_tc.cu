@@ -129,6 +129,7 @@ __device__ __forceinline__ void add_delta(f32x2 (&S)[16], uint32_t d, float2 dec
 // a warp per (chunk, head), four tokens per lane
 __global__ void __launch_bounds__(256) linear_decay_kernel(LinArgs a, Decay *rec, long long n)
 {
+    asm volatile("griddepcontrol.launch_dependents;");   // the walk that follows may set itself up meanwhile
     const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (id >= n) return;
@@ -386,6 +387,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
     } else if (warp == W_TMA) {
         // ---------------------------------------------------------- TMA: Q, K and V are refilled as each is free
         if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");   // the decay records are complete
             const Decay *decay = f.decay + (size_t)(lin_first_slot(a, pc.s, pc.t0, C) + pc.j * (f.sp.seg / C)) * a.H + h;
             for (int c = 0; c < n; ++c) {
                 const int st = c & 1, tok = tok0 + c * C;
@@ -605,6 +607,7 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
         }
     } else if (warp == W_TMA) {
         if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             for (int c = 0; c < n; ++c) {
                 const int st = c & 1, tok = tok0 + chunk(c) * C;
                 if (c + 2 < n) {              // (as in the forward)
@@ -710,18 +713,34 @@ cudaError_t setup(K kern, size_t smem, int threads) {
     return kernel_setup(reinterpret_cast<const void *>(kern), smem, threads, false, &ks);
 }
 
+// `early`: right behind the decay launch; the CTAs may then start before it is done (they wait for it before they read
+// its records, and touch nothing else that it does)
+template <typename K, typename A>
+cudaError_t launch(K kern, long long grid, int threads, size_t smem, const A &args, bool early, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args);
+}
+
 template <bool REV, bool TOTALS>
-cudaError_t states(const StateArgs &f, cudaStream_t st) {
+cudaError_t states(const StateArgs &f, bool early, cudaStream_t st) {
     auto kern = f.a.dk > 64 ? linear_state_kernel<REV, TOTALS, 2> : linear_state_kernel<REV, TOTALS, 1>;
     const cudaError_t e = setup(kern, StateSmem::TOTAL, NT_S);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(slots(f.a, f.piece) * f.a.H * tiles_of(f.a)), NT_S, StateSmem::TOTAL, st>>>(f);
-    return cudaGetLastError();
+    return launch(kern, slots(f.a, f.piece) * f.a.H * tiles_of(f.a), NT_S, StateSmem::TOTAL, f, early, st);
 }
 
 // totals of the earlier segments into ws, if the sequences are cut
 template <bool REV>
-cudaError_t totals(StateArgs f, uint8_t *ws, Split *sp, cudaStream_t st) {
+cudaError_t totals(StateArgs f, uint8_t *ws, Split *sp, bool early, cudaStream_t st) {
     split_of(f.a, &sp->seg, &sp->sub);
     sp->U = nullptr;
     sp->dec = nullptr;
@@ -736,7 +755,7 @@ cudaError_t totals(StateArgs f, uint8_t *ws, Split *sp, cudaStream_t st) {
     f.last = nullptr;
     sp->U = U;
     sp->dec = dec;
-    return states<REV, true>(f, st);
+    return states<REV, true>(f, early, st);
 }
 
 }  // namespace
@@ -759,12 +778,11 @@ cudaError_t launch_linear_tc(const LinArgs &a, void *workspace, cudaStream_t st)
     s.ty = f.tv;
     s.decay = f.decay = static_cast<const Decay *>(workspace);
     cudaError_t e = decays(a, workspace, st);
-    if (e == cudaSuccess) e = totals<false>(s, static_cast<uint8_t *>(workspace) + decay_bytes(a), &f.sp, st);
+    if (e == cudaSuccess) e = totals<false>(s, static_cast<uint8_t *>(workspace) + decay_bytes(a), &f.sp, true, st);
     auto kern = a.dk > 64 ? linear_forward_kernel<2> : linear_forward_kernel<1>;
     if (e == cudaSuccess) e = setup(kern, FwdSmem::TOTAL, NT_F);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(slots(a, f.sp.seg) * a.H * tiles_of(a)), NT_F, FwdSmem::TOTAL, st>>>(f);
-    return cudaGetLastError();
+    return launch(kern, slots(a, f.sp.seg) * a.H * tiles_of(a), NT_F, FwdSmem::TOTAL, f, !is_split(a, f.sp.seg), st);
 }
 
 namespace lin {
@@ -795,22 +813,22 @@ cudaError_t launch_states(const LinBwdArgs &b, void *workspace, States *out, cud
     f.decay = out->decay;
     // forwards: the states at the chunks' starts
     if (!make_token_map(&f.tx, a.k, a.dk, a.H, a.ntok) || !make_token_map(&f.ty, a.v, a.dv, a.H, a.ntok)) return cudaErrorInvalidValue;
-    e = totals<false>(f, tot, &f.sp, st);
+    e = totals<false>(f, tot, &f.sp, true, st);
     if (e != cudaSuccess) return e;
     f.piece = f.sp.seg;
     f.tiles = S;
     f.first = a.S0;
-    e = states<false, false>(f, st);
+    e = states<false, false>(f, !is_split(a, f.sp.seg), st);
     if (e != cudaSuccess) return e;
     // backwards: the state's gradient at their ends
     if (!make_token_map(&f.tx, a.q, a.dk, a.H, a.ntok) || !make_token_map(&f.ty, b.d_o, a.dv, a.H, a.ntok)) return cudaErrorInvalidValue;
-    e = totals<true>(f, tot, &f.sp, st);
+    e = totals<true>(f, tot, &f.sp, false, st);
     if (e != cudaSuccess) return e;
     f.piece = f.sp.seg;
     f.tiles = R;
     f.first = b.dS_T;
     f.last = b.dS0;
-    return states<true, false>(f, st);
+    return states<true, false>(f, false, st);
 }
 
 }  // namespace lin
