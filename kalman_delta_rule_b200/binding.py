@@ -79,6 +79,8 @@ _SIGS = {
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libkdn.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -372,93 +374,125 @@ def gain_scan(k, alpha, sigma, r, cu_seqlens=None, P0=None, mu: float = 1.0, chu
 
 
 # ------------------------------------------------------------------ linear attention, layer norm
-_DTYPES = {"torch.bfloat16": KDN_DTYPE_BF16, "torch.float32": KDN_DTYPE_F32}
+# These wrappers serve single-token decoding too, where the launch takes a few microseconds: what they do per call
+# is kept short (one pass of checks, no context managers unless another device or stream is asked for).
+_mod = None
+_raw_stream = None   # device index -> handle of its current stream
+
+
+def _cuda():
+    """torch, once a CUDA device has been seen."""
+    global _mod, _raw_stream
+    if _mod is None:
+        torch = _torch()
+        # (a Stream object costs several microseconds; torch's own code generators read the handle this way)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _mod = torch
+    return _mod
+
+
+def _type_of(torch, name, t):
+    if t.dtype is torch.bfloat16:
+        return KDN_DTYPE_BF16
+    if t.dtype is torch.float32:
+        return KDN_DTYPE_F32
+    raise TypeError(f"{name} is {t.dtype} (float32 or bfloat16 expected)")
 
 
 def _expect(name, t, shape, dtype, device):
     """Raise unless ``t`` is a contiguous tensor of this shape, type and device."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}, expected {device} (CUDA)")
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _type_of(name, t):
-    code = _DTYPES.get(str(t.dtype))
-    if code is None:
-        raise TypeError(f"{name} is {t.dtype} (float32 or bfloat16 expected)")
-    return code
+def _device_of(name, t):
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} is on {dev}, expected a CUDA device")
+    return dev
 
 
-def _dptr(t):
-    return None if t is None else t.data_ptr()
+def _launch(torch, dev, stream, fn):
+    """fn(stream handle) with the tensors' device and the caller's stream current: outputs and workspace come from
+    that stream's allocator, and the kernels are launched on it.  ``stream`` None is that device's current one."""
+    if stream is None:
+        if torch.cuda.current_device() == dev.index:
+            return fn(_raw_stream(dev.index) or None)
+        with torch.cuda.device(dev):
+            return fn(_raw_stream(dev.index) or None)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return fn(stream.cuda_stream or None)
 
 
-class _On:
-    """The tensors' device and the caller's stream made current: outputs and workspace come from that
-    stream's allocator, and the kernels are launched on it.  ``stream`` None is that device's current one."""
+def _work(torch, name, workspace, need, dev):
+    """(the caller's workspace, or a new one of ``need`` bytes; its pointer; its bytes)"""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"{name}: the workspace must be contiguous and on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
-    def __init__(self, torch, device, stream):
-        self.torch, self.device, self.stream = torch, device, stream
 
-    def __enter__(self):
-        torch = self.torch
-        self.ctx = None
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError(f"stream is on {self.stream.device}, the tensors on {self.device}")
-            self.ctx = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != self.device.index:
-            self.ctx = torch.cuda.device(self.device)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream()
-        return s.cuda_stream or None
+_sizes = {}   # workspace bytes by problem: a function of the sizes alone
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _need(fn, p, packed):
+    key = (fn, p.B, p.T, p.H, p.d_k, p.d_v, p.num_seqs, packed, p.in_dtype)
+    n = _sizes.get(key)
+    if n is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        n = _sizes[key] = fn(p)
+    return n
 
 
 def _linear_problem(q, k, v, g, cu_seqlens, scale):
-    torch = _torch()
+    torch = _mod or _cuda()
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be [B, T, H, d]")
-    B, T, H, dk = q.shape
-    dev = q.device
-    p = kdn_linear_problem_t()
-    p.in_dtype = _type_of("q", q)
-    _expect("q", q, q.shape, q.dtype, dev)
-    _expect("k", k, q.shape, q.dtype, dev)
-    _expect("v", v, (B, T, H, v.shape[-1]), q.dtype, dev)
-    p.B, p.T, p.H, p.d_k, p.d_v, p.scale = B, T, H, dk, v.shape[-1], float(scale)
-    p.num_seqs = B
+    shape, dtype, dev = q.shape, q.dtype, _device_of("q", q)
+    B, T, H, dk = shape
+    dv = v.shape[3]
+    code = _type_of(torch, "q", q)
+    _expect("q", q, shape, dtype, dev)
+    _expect("k", k, shape, dtype, dev)
+    _expect("v", v, (B, T, H, dv), dtype, dev)
+    n, cu = B, None
     if cu_seqlens is not None:
-        _expect("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32, dev)
-        if cu_seqlens.numel() < 1:
-            raise ValueError("cu_seqlens needs at least one entry")
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must be one-dimensional, with at least one entry")
+        _expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
         if B != 1:
             raise ValueError("packed sequences need B = 1")
-        p.num_seqs = cu_seqlens.numel() - 1
-        # without sequences the pointer would be all that marks the problem as packed
-        p.cu_seqlens = cu_seqlens.data_ptr()
+        n, cu = cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
+    decay, gp = KDN_DECAY_NONE, None
     if g is not None:
-        p.decay = KDN_DECAY_HEAD if g.dim() == 1 else KDN_DECAY_TOKEN
-        _expect("g", g, (H,) if g.dim() == 1 else (B, T, H), torch.float32, dev)
-    return torch, p
+        if g.dim() == 1:
+            decay = KDN_DECAY_HEAD
+            _expect("g", g, (H,), torch.float32, dev)
+        else:
+            decay = KDN_DECAY_TOKEN
+            _expect("g", g, (B, T, H), torch.float32, dev)
+        gp = g.data_ptr()
+    return torch, dev, kdn_linear_problem_t(B, T, H, dk, dv, cu, n, code, scale, decay), (n, H, dk, dv), gp
 
 
-def _linear_state(torch, name, t, p, dev):
-    if t is not None:
-        _expect(name, t, (p.num_seqs, p.H, p.d_k, p.d_v), torch.float32, dev)
-
-
-def _bytes(torch, n, dev):
-    return torch.empty(n, dtype=torch.uint8, device=dev)
+def _state_ptr(torch, name, t, shape, dev):
+    if t is None:
+        return None
+    _expect(name, t, shape, torch.float32, dev)
+    return t.data_ptr()
 
 
 def linear_forward(q, k, v, g=None, cu_seqlens=None, S0=None, scale: float = 1.0, o=None, S_out=None,
@@ -469,41 +503,47 @@ def linear_forward(q, k, v, g=None, cu_seqlens=None, S0=None, scale: float = 1.0
     q, k [B,T,H,dk] and v [B,T,H,dv] in bf16 or fp32; g the fp32 log decay, [B,T,H], [H] or None (no
     decay); varlen: B = 1 with int32 cu_seqlens; S0 [N,H,dk,dv] fp32.  Returns (o, S_out); outputs
     and workspace are allocated when not given (S_out stays None without ``want_state``)."""
-    torch, p = _linear_problem(q, k, v, g, cu_seqlens, scale)
-    dev = q.device
-    _linear_state(torch, "S0", S0, p, dev)
-    with _On(torch, dev, stream) as handle:
-        if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
-        else:
-            _expect("o", o, v.shape, q.dtype, dev)
-        if S_out is None and want_state:
-            S_out = torch.empty((p.num_seqs, p.H, p.d_k, p.d_v), dtype=torch.float32, device=dev)
-        else:
-            _linear_state(torch, "S_out", S_out, p, dev)
-        if workspace is None:
-            workspace = _bytes(torch, kdn_linear_workspace_size(p), dev)
-        st = kdn_linear_forward(p, _dptr(q), _dptr(k), _dptr(v), _dptr(g), _dptr(S0), _dptr(o), _dptr(S_out),
-                                _ptr(workspace), workspace.numel() * workspace.element_size(), handle)
-    _check(st, "kdn_linear_forward")
-    return o, S_out
+    torch, dev, p, states, gp = _linear_problem(q, k, v, g, cu_seqlens, scale)
+    s0 = _state_ptr(torch, "S0", S0, states, dev)
+    if o is not None:
+        _expect("o", o, v.shape, q.dtype, dev)
+    so = _state_ptr(torch, "S_out", S_out, states, dev)
+
+    def run(handle):
+        out = torch.empty_like(v) if o is None else o
+        last, lp = S_out, so
+        if last is None and want_state:
+            last = torch.empty(states, dtype=torch.float32, device=dev)
+            lp = last.data_ptr()
+        ws, wp, wb = _work(torch, "linear_forward", workspace, _need(kdn_linear_workspace_size, p, cu_seqlens is not None), dev)
+        st = _lib.kdn_linear_forward(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, s0, out.data_ptr(), lp, wp,
+                                     wb, handle)
+        if st != KDN_OK:
+            raise KdnError(st, "kdn_linear_forward")
+        return out, last
+
+    load()
+    return _launch(torch, dev, stream, run)
 
 
 def linear_decode_tokens(q, k, v, g, S, scale: float = 1.0, o=None, stream=None):
     """n tokens per sequence of the recurrent form in one launch on [N, n, H, d] token tensors
     (kdn_linear_decode_tokens); g [N, n, H], [H] or None; S [N,H,dk,dv] fp32, updated in place."""
-    torch, p = _linear_problem(q, k, v, g, None, scale)
-    dev = q.device
-    _linear_state(torch, "S", S, p, dev)
-    with _On(torch, dev, stream) as handle:
-        if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
-        else:
-            _expect("o", o, v.shape, q.dtype, dev)
-        st = kdn_linear_decode_tokens(p.B, p.T, p.H, p.d_k, p.d_v, p.in_dtype, p.scale, p.decay, _dptr(q), _dptr(k),
-                                      _dptr(v), _dptr(g), _dptr(S), _dptr(o), handle)
-    _check(st, "kdn_linear_decode_tokens")
-    return o
+    torch, dev, p, states, gp = _linear_problem(q, k, v, g, None, scale)
+    _expect("S", S, states, torch.float32, dev)
+    if o is not None:
+        _expect("o", o, v.shape, q.dtype, dev)
+
+    def run(handle):
+        out = torch.empty_like(v) if o is None else o
+        st = _lib.kdn_linear_decode_tokens(p.B, p.T, p.H, p.d_k, p.d_v, p.in_dtype, p.scale, p.decay, q.data_ptr(), k.data_ptr(),
+                                           v.data_ptr(), gp, S.data_ptr(), out.data_ptr(), handle)
+        if st != KDN_OK:
+            raise KdnError(st, "kdn_linear_decode_tokens")
+        return out
+
+    load()
+    return _launch(torch, dev, stream, run)
 
 
 def linear_decode_step(q, k, v, g, S, scale: float = 1.0, o=None, stream=None):
@@ -521,25 +561,30 @@ def linear_backward(q, k, v, g, d_o, cu_seqlens=None, S0=None, dS=None, scale: f
 
     Returns a dict: dq, dk, dv (shapes and type of q, k, v), with a decay dg (fp32, shape of g), and with
     ``want_initial`` dS0 [N,H,dk,dv] fp32.  The workspace is allocated when not given."""
-    torch, p = _linear_problem(q, k, v, g, cu_seqlens, scale)
-    dev = q.device
+    torch, dev, p, states, gp = _linear_problem(q, k, v, g, cu_seqlens, scale)
     _expect("d_o", d_o, v.shape, q.dtype, dev)
-    _linear_state(torch, "S0", S0, p, dev)
-    _linear_state(torch, "dS", dS, p, dev)
-    with _On(torch, dev, stream) as handle:
-        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
+    s0, ds = _state_ptr(torch, "S0", S0, states, dev), _state_ptr(torch, "dS", dS, states, dev)
+
+    def run(handle):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        out = {"dq": dq, "dk": dk, "dv": dv}
+        dgp = dsp = None
         if g is not None:
             out["dg"] = torch.empty_like(g)
+            dgp = out["dg"].data_ptr()
         if want_initial:
-            out["dS0"] = torch.empty((p.num_seqs, p.H, p.d_k, p.d_v), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = _bytes(torch, kdn_linear_backward_workspace_size(p), dev)
-        st = kdn_linear_backward(p, _dptr(q), _dptr(k), _dptr(v), _dptr(g), _dptr(S0), _dptr(d_o), _dptr(dS),
-                                 _dptr(out["dq"]), _dptr(out["dk"]), _dptr(out["dv"]), _dptr(out.get("dg")),
-                                 _dptr(out.get("dS0")), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                 handle)
-    _check(st, "kdn_linear_backward")
-    return out
+            out["dS0"] = torch.empty(states, dtype=torch.float32, device=dev)
+            dsp = out["dS0"].data_ptr()
+        ws, wp, wb = _work(torch, "linear_backward", workspace,
+                           _need(kdn_linear_backward_workspace_size, p, cu_seqlens is not None), dev)
+        st = _lib.kdn_linear_backward(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, s0, d_o.data_ptr(), ds,
+                                      dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dgp, dsp, wp, wb, handle)
+        if st != KDN_OK:
+            raise KdnError(st, "kdn_linear_backward")
+        return out
+
+    load()
+    return _launch(torch, dev, stream, run)
 
 
 def _norm_rows(x, weight):
@@ -558,54 +603,75 @@ def _norm_rows(x, weight):
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, y=None, stream=None):
     """Layer norm over the last axis (kdn_layer_norm); returns (y, mean, rstd), mean and rstd fp32 of
     x.shape[:-1].  weight, bias: fp32 [d], or [G, d] for x [..., G, d] (a row for each head), or None."""
-    torch = _torch()
-    code = _type_of("x", x)
-    dev = x.device
+    torch = _mod or _cuda()
+    code = _type_of(torch, "x", x)
+    dev = _device_of("x", x)
     _expect("x", x, x.shape, x.dtype, dev)
-    n, G, d = _norm_rows(x, weight if weight is not None else bias)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _expect(name, t, (G, d) if t.dim() == 2 else (d,), torch.float32, dev)
-            if t.numel() != G * d:
-                raise ValueError("weight and bias must have the same shape")
-    with _On(torch, dev, stream) as handle:
-        if y is None:
-            y = torch.empty_like(x)
-        else:
-            _expect("y", y, x.shape, x.dtype, dev)
+    param = weight if weight is not None else bias
+    n, G, d = _norm_rows(x, param)
+    wp = bp = None
+    if param is not None:
+        shape = (G, d) if param.dim() == 2 else (d,)
+        if weight is not None:
+            _expect("weight", weight, shape, torch.float32, dev)
+            wp = weight.data_ptr()
+        if bias is not None:
+            _expect("bias", bias, shape, torch.float32, dev)
+            bp = bias.data_ptr()
+    if y is not None:
+        _expect("y", y, x.shape, x.dtype, dev)
+
+    def run(handle):
+        out = torch.empty_like(x) if y is None else y
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
         rstd = torch.empty_like(mean)
-        st = kdn_layer_norm(n, G, d, code, float(eps), _dptr(x), _dptr(weight), _dptr(bias), _dptr(y), _dptr(mean),
-                            _dptr(rstd), handle)
-    _check(st, "kdn_layer_norm")
-    return y, mean, rstd
+        st = _lib.kdn_layer_norm(n, G, d, code, eps, x.data_ptr(), wp, bp, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), handle)
+        if st != KDN_OK:
+            raise KdnError(st, "kdn_layer_norm")
+        return out, mean, rstd
+
+    load()
+    return _launch(torch, dev, stream, run)
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, workspace=None, stream=None):
     """Gradients of <y, dy> for ``layer_norm`` (kdn_layer_norm_backward), mean and rstd as it returned
     them: a dict of dx and, with a weight, dweight and dbias (fp32, the weight's shape)."""
-    torch = _torch()
-    code = _type_of("x", x)
-    dev = x.device
-    _expect("x", x, x.shape, x.dtype, dev)
-    _expect("dy", dy, x.shape, x.dtype, dev)
+    torch = _mod or _cuda()
+    code = _type_of(torch, "x", x)
+    dev = _device_of("x", x)
+    shape = x.shape
+    _expect("x", x, shape, x.dtype, dev)
+    _expect("dy", dy, shape, x.dtype, dev)
     n, G, d = _norm_rows(x, weight)
+    wp = None
     if weight is not None:
         _expect("weight", weight, (G, d) if weight.dim() == 2 else (d,), torch.float32, dev)
-    _expect("mean", mean, x.shape[:-1], torch.float32, dev)
-    _expect("rstd", rstd, x.shape[:-1], torch.float32, dev)
-    with _On(torch, dev, stream) as handle:
-        out = {"dx": torch.empty_like(x)}
+        wp = weight.data_ptr()
+    _expect("mean", mean, shape[:-1], torch.float32, dev)
+    _expect("rstd", rstd, shape[:-1], torch.float32, dev)
+
+    def run(handle):
+        dx = torch.empty_like(x)
+        out = {"dx": dx}
+        dwp = dbp = sp = None
+        sb = 0
         if weight is not None:
             out["dweight"], out["dbias"] = torch.empty_like(weight), torch.empty_like(weight)
-            if workspace is None:
-                workspace = _bytes(torch, kdn_layer_norm_backward_workspace_size(n, G, d), dev)
-        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = kdn_layer_norm_backward(n, G, d, code, _dptr(dy), _dptr(x), _dptr(weight), _dptr(mean), _dptr(rstd),
-                                     _dptr(out["dx"]), _dptr(out.get("dweight")), _dptr(out.get("dbias")),
-                                     _ptr(workspace), wbytes, handle)
-    _check(st, "kdn_layer_norm_backward")
-    return out
+            dwp, dbp = out["dweight"].data_ptr(), out["dbias"].data_ptr()
+            key = ("norm", n, G, d)
+            need = _sizes.get(key)
+            if need is None:
+                need = _sizes[key] = kdn_layer_norm_backward_workspace_size(n, G, d)
+            ws, sp, sb = _work(torch, "layer_norm_backward", workspace, need, dev)
+        st = _lib.kdn_layer_norm_backward(n, G, d, code, dy.data_ptr(), x.data_ptr(), wp, mean.data_ptr(), rstd.data_ptr(),
+                                          dx.data_ptr(), dwp, dbp, sp, sb, handle)
+        if st != KDN_OK:
+            raise KdnError(st, "kdn_layer_norm_backward")
+        return out
+
+    load()
+    return _launch(torch, dev, stream, run)
 
 
 PATH_NAMES = {0: "recurrent", 1: "chunk_fp32", 3: "chunk_tcgen05_two_phase"}
