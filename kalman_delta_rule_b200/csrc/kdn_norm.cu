@@ -6,7 +6,9 @@
 // A row is held in the registers of LPR threads, EPL elements each, so x (and dy) is read once and
 // the variance is the mean of squared deviations from a mean that is already known.  LPR <= 32: a row
 // per part of a warp, sums by shuffles; LPR = 256 or 512: a row per CTA.  All sums are fp32.
-// Both directions are bound by HBM: the forward moves 2 d elements per row, the backward 3 d.
+// Both directions are bound by HBM: the forward moves 2 d elements per row, the backward 3 d.  A row's
+// reductions are a chain of latencies, so the next row's loads are issued before them, and the launch has as
+// many CTAs as are resident at once (a second, partial wave cost up to a third).
 //
 // dw and db: a row's threads always own the same columns of the same group, so each keeps its columns'
 // two sums in registers over all the rows it walks; the CTA's rows join in shared memory, and the CTA
@@ -21,10 +23,17 @@ namespace {
 
 constexpr int kMaxBlocks = 148 * 8;   // CTAs of a launch (backward: shares of dw, db in the workspace)
 
+// VEC elements as they are in memory (16 bytes, or one element), and widened
+template <typename T, int VEC> struct Raw { typedef uint4 type; };
+template <> struct Raw<float, 1> { typedef float type; };
+template <> struct Raw<bf16, 1> { typedef unsigned short type; };
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(float *dst, const T *src) {
+__device__ __forceinline__ typename Raw<T, VEC>::type load_raw(const T *src) {
+    return __ldg(reinterpret_cast<const typename Raw<T, VEC>::type *>(src));
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void widen(float *dst, const typename Raw<T, VEC>::type &u) {
     if constexpr (VEC == 8) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src));
         const unsigned w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -32,10 +41,12 @@ __device__ __forceinline__ void load_vec(float *dst, const T *src) {
             dst[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     } else if constexpr (VEC == 4) {
-        const float4 f = ldf4(src);
-        dst[0] = f.x; dst[1] = f.y; dst[2] = f.z; dst[3] = f.w;
+        dst[0] = __uint_as_float(u.x); dst[1] = __uint_as_float(u.y);
+        dst[2] = __uint_as_float(u.z); dst[3] = __uint_as_float(u.w);
+    } else if constexpr (sizeof(T) == 4) {
+        dst[0] = u;
     } else {
-        dst[0] = ldf(src);
+        dst[0] = __uint_as_float((unsigned)u << 16);
     }
 }
 template <typename T, int VEC>
@@ -62,31 +73,54 @@ struct Shape {
     static constexpr int ROWS = NT / LPR;                // rows of a CTA at a time
 };
 
-// sum over the LPR threads of a row; every one of them gets it
-template <int LPR>
-__device__ __forceinline__ float row_sum(float x, float *red) {
+// N sums over the LPR threads of a row; every one of them gets them.  Over a CTA: one barrier, on two buffers in
+// turn (who writes a buffer again has passed a barrier that its readers reached after reading)
+template <int LPR, int N>
+struct RowSum {
+    float (*red)[N][LPR > 32 ? LPR / 32 : 1];   // [2][N][warps]
+    int turn = 0;
+    __device__ __forceinline__ void operator()(float (&x)[N]) {
 #pragma unroll
-    for (int o = (LPR < 32 ? LPR : 32) / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if constexpr (LPR > 32) {
-        __syncthreads();       // the previous sum has been read
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-        __syncthreads();
-        x = 0.f;
+        for (int o = (LPR < 32 ? LPR : 32) / 2; o > 0; o >>= 1)
 #pragma unroll
-        for (int w = 0; w < LPR / 32; ++w) x += red[w];
+            for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+        if constexpr (LPR > 32) {
+            turn ^= 1;
+            if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) red[turn][i][threadIdx.x >> 5] = x[i];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                x[i] = 0.f;
+#pragma unroll
+                for (int w = 0; w < LPR / 32; ++w) x[i] += red[turn][i][w];
+            }
+        }
     }
-    return x;
-}
+};
 
-// A CTA serves one group; its rows are i = first, first + step, ... of the n rows of that group.
+// the rows of a group that a thread's place in its CTA walks: i = first, first + step, ... < n (all threads of a CTA
+// take the same number of turns: the sums over a row shuffle or synchronise)
+template <int LPR>
+struct Rows {
+    long long first, step;
+    __device__ __forceinline__ Rows(const NormArgs &a)
+        : first((long long)(blockIdx.x / a.G) * Shape<LPR>::ROWS), step((long long)(gridDim.x / a.G) * Shape<LPR>::ROWS) {}
+};
+
+// A CTA serves one group.
 template <typename T, int VEC, int LPR, int EPL>
 __global__ void __launch_bounds__(Shape<LPR>::NT) norm_kernel(NormArgs a)
 {
-    constexpr int ROWS = Shape<LPR>::ROWS, NV = EPL / VEC;
-    __shared__ float red[LPR > 32 ? LPR / 32 : 1];
-    const int g = blockIdx.x % a.G, lane = threadIdx.x % LPR;
-    const long long step = (long long)(gridDim.x / a.G) * ROWS;
-    const float width = (float)a.d;   // a division, not a product with 1 / d: a constant row's mean is its value
+    constexpr int NV = EPL / VEC;
+    typedef typename Raw<T, VEC>::type raw_t;
+    __shared__ float red[2][1][LPR > 32 ? LPR / 32 : 1];
+    RowSum<LPR, 1> sum{red};
+    const int g = blockIdx.x % a.G, lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
+    const Rows<LPR> rows(a);
+    const float width = (float)a.d, inv = 1.f / width;
     float w[EPL], b[EPL];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -97,39 +131,40 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_kernel(NormArgs a)
             b[j * VEC + e] = a.bias && c < a.d ? __ldg(a.bias + (size_t)g * a.d + c + e) : 0.f;
         }
     }
-    // all threads of a CTA take the same number of turns: the sums over a row shuffle or synchronise
-    for (long long i0 = (long long)(blockIdx.x / a.G) * ROWS; i0 < a.n; i0 += step) {
-        const long long i = i0 + threadIdx.x / LPR;
-        const bool live = i < a.n;
-        const size_t row = (size_t)(live ? i : 0) * a.G + g;
-        const T *x = static_cast<const T *>(a.x) + row * a.d;
-        float v[EPL];
-        float s = 0.f;
+    raw_t next[NV] = {};
+    auto fetch = [&](long long i0) {
+        const long long i = i0 + sub;
+        if (i >= a.n) return;
+        const T *x = static_cast<const T *>(a.x) + ((size_t)i * a.G + g) * a.d;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + lane) * VEC;
-            if (live && c < a.d) {
-                load_vec<T, VEC>(v + j * VEC, x + c);
-            } else {
+        for (int j = 0; j < NV; ++j)
+            if ((j * LPR + lane) * VEC < a.d) next[j] = load_raw<T, VEC>(x + (j * LPR + lane) * VEC);
+    };
+    fetch(rows.first);
+    for (long long i0 = rows.first; i0 < a.n; i0 += rows.step) {
+        const long long i = i0 + sub;
+        float v[EPL], s[1] = {0.f};
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) v[j * VEC + e] = 0.f;
-            }
-        }
+        for (int j = 0; j < NV; ++j) widen<T, VEC>(v + j * VEC, next[j]);   // (zero behind the row's end)
+        fetch(i0 + rows.step);
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) s += v[e];
-        const float mean = row_sum<LPR>(s, red) / width;
-        s = 0.f;
+        for (int e = 0; e < EPL; ++e) s[0] += v[e];
+        sum(s);
+        const float mean = s[0] / width;      // (not a product with 1 / d: a constant row's mean is its value)
+        s[0] = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const bool in = (j * LPR + lane) * VEC < a.d;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 v[j * VEC + e] -= mean;
-                if (in) s = fmaf(v[j * VEC + e], v[j * VEC + e], s);
+                if (in) s[0] = fmaf(v[j * VEC + e], v[j * VEC + e], s[0]);
             }
         }
-        const float rstd = rsqrtf(row_sum<LPR>(s, red) / width + a.eps);
-        if (!live) continue;
+        sum(s);
+        const float rstd = rsqrtf(fmaf(s[0], inv, a.eps));
+        if (i >= a.n) continue;
+        const size_t row = (size_t)i * a.G + g;
         T *y = static_cast<T *>(a.y) + row * a.d;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -151,12 +186,13 @@ template <typename T, int VEC, int LPR, int EPL>
 __global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs a)
 {
     constexpr int ROWS = Shape<LPR>::ROWS, NV = EPL / VEC;
-    __shared__ float red[LPR > 32 ? LPR / 32 : 1];
+    typedef typename Raw<T, VEC>::type raw_t;
+    __shared__ float red[2][2][LPR > 32 ? LPR / 32 : 1];
     __shared__ float join[ROWS > 1 ? ROWS : 1][ROWS > 1 ? LPR * VEC : 1];
+    RowSum<LPR, 2> sum{red};
     const int g = blockIdx.x % a.G, lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
-    const long long step = (long long)(gridDim.x / a.G) * ROWS;
-    const float width = (float)a.d;
-    const bool params = a.part != nullptr;
+    const Rows<LPR> rows(a);
+    const float inv = 1.f / (float)a.d;
     float w[EPL], dw[EPL], db[EPL];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -167,51 +203,65 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs 
             dw[j * VEC + e] = db[j * VEC + e] = 0.f;
         }
     }
-    for (long long i0 = (long long)(blockIdx.x / a.G) * ROWS; i0 < a.n; i0 += step) {
+    // a place without an element or a row holds zeros: dy's make every term of it vanish
+    raw_t next_x[NV] = {}, next_dy[NV] = {};
+    float next_mean = 0.f, next_rstd = 0.f;
+    auto fetch = [&](long long i0) {
         const long long i = i0 + sub;
-        const bool live = i < a.n;
-        const size_t row = (size_t)(live ? i : 0) * a.G + g;
+        if (i >= a.n) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) next_x[j] = next_dy[j] = raw_t();
+            next_mean = next_rstd = 0.f;
+            return;
+        }
+        const size_t row = (size_t)i * a.G + g;
         const T *x = static_cast<const T *>(a.x) + row * a.d, *dy = static_cast<const T *>(a.dy) + row * a.d;
-        float xh[EPL], u[EPL];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + lane) * VEC;
-            if (live && c < a.d) {
-                load_vec<T, VEC>(xh + j * VEC, x + c);
-                load_vec<T, VEC>(u + j * VEC, dy + c);
+            if ((j * LPR + lane) * VEC < a.d) {
+                next_x[j] = load_raw<T, VEC>(x + (j * LPR + lane) * VEC);
+                next_dy[j] = load_raw<T, VEC>(dy + (j * LPR + lane) * VEC);
             }
         }
-        const float mean = live ? __ldg(a.mean + row) : 0.f, rstd = live ? __ldg(a.rstd + row) : 0.f;
-        float s1 = 0.f, s2 = 0.f;
+        next_mean = __ldg(a.mean + row);
+        next_rstd = __ldg(a.rstd + row);
+    };
+    fetch(rows.first);
+    for (long long i0 = rows.first; i0 < a.n; i0 += rows.step) {
+        const long long i = i0 + sub;
+        float xh[EPL], u[EPL], s[2] = {0.f, 0.f};
+        const float mean = next_mean, rstd = next_rstd;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool in = live && (j * LPR + lane) * VEC < a.d;
-#pragma unroll
-            for (int e = j * VEC; e < (j + 1) * VEC; ++e) {
-                xh[e] = in ? (xh[e] - mean) * rstd : 0.f;
-                u[e] = in ? u[e] : 0.f;
-                dw[e] = fmaf(xh[e], u[e], dw[e]);
-                db[e] += u[e];
-                u[e] *= w[e];
-                s1 += u[e];
-                s2 = fmaf(u[e], xh[e], s2);
-            }
+            widen<T, VEC>(xh + j * VEC, next_x[j]);
+            widen<T, VEC>(u + j * VEC, next_dy[j]);
         }
-        s1 = row_sum<LPR>(s1, red) / width;
-        s2 = row_sum<LPR>(s2, red) / width;
-        if (!live) continue;
-        T *dx = static_cast<T *>(a.dx) + row * a.d;
+        fetch(i0 + rows.step);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            xh[e] = (xh[e] - mean) * rstd;
+            dw[e] = fmaf(xh[e], u[e], dw[e]);
+            db[e] += u[e];
+            u[e] *= w[e];
+            s[0] += u[e];
+            s[1] = fmaf(u[e], xh[e], s[1]);
+        }
+        sum(s);
+        if (i >= a.n) continue;
+        const float m1 = s[0] * inv, m2 = s[1] * inv;
+        T *dx = static_cast<T *>(a.dx) + ((size_t)i * a.G + g) * a.d;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * LPR + lane) * VEC;
             if (c >= a.d) continue;
             float o[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = rstd * (u[j * VEC + e] - s1 - xh[j * VEC + e] * s2);
+            for (int e = 0; e < VEC; ++e) o[e] = rstd * (u[j * VEC + e] - m1 - xh[j * VEC + e] * m2);
             store_vec<T, VEC>(dx + c, o);
         }
     }
-    if (!params) return;
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (!a.part) return;
     // the CTA's share: [CTA][2][d]
     float *part = a.part + (size_t)blockIdx.x * 2 * a.d;
 #pragma unroll
@@ -240,59 +290,75 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs 
     }
 }
 
-// dw, db [G, d] from the CTAs' shares: thread = (column, one of 8 parts of the CTAs)
-__global__ void __launch_bounds__(256) norm_params_kernel(NormArgs a, int blocks)
+// dw, db [G, d] from the CTAs' shares: thread = (column, one of 32 parts of the CTAs)
+__global__ void __launch_bounds__(1024) norm_params_kernel(NormArgs a, int blocks)
 {
-    __shared__ float red[2][8][32];
-    const int g = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+    __shared__ float red[2][32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // (launched while the rows' kernel runs out)
+    const int g = blockIdx.y, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, part = threadIdx.x >> 5;
     float s0 = 0.f, s1 = 0.f;
-    if (c < a.d)
-        for (int b = g + part * a.G; b < blocks; b += 8 * a.G) {
-            s0 += a.part[(size_t)b * 2 * a.d + c];
-            s1 += a.part[(size_t)b * 2 * a.d + a.d + c];
+    if (c < a.d) {
+#pragma unroll 4
+        for (int b = g + part * a.G; b < blocks; b += 32 * a.G) {
+            s0 += __ldg(a.part + (size_t)b * 2 * a.d + c);
+            s1 += __ldg(a.part + (size_t)b * 2 * a.d + a.d + c);
         }
-    red[0][part][threadIdx.x & 31] = s0;
-    red[1][part][threadIdx.x & 31] = s1;
+    }
+    red[0][part][lane] = s0;
+    red[1][part][lane] = s1;
     __syncthreads();
-    if (part < 2 && c < a.d) {
-        float s = 0.f;
-#pragma unroll
-        for (int p = 0; p < 8; ++p) s += red[part][p][threadIdx.x & 31];
-        float *dst = part ? a.dbias : a.dweight;
-        if (dst) dst[(size_t)g * a.d + c] = s;
+    // warp w joins the parts of column w
+    s0 = warp_sum(red[0][lane][part]);
+    s1 = warp_sum(red[1][lane][part]);
+    const int cw = blockIdx.x * 32 + part;
+    if (lane == 0 && cw < a.d) {
+        if (a.dweight) a.dweight[(size_t)g * a.d + cw] = s0;
+        if (a.dbias) a.dbias[(size_t)g * a.d + cw] = s1;
     }
 }
 
-// CTAs of a launch: a multiple of the groups, no more than the rows need, at most `most`
-int blocks_for(long long n, int G, int rows, int most) {
-    const long long need = (n + rows - 1) / rows;
-    long long per = most / G;
+// CTAs of a launch: as many as are resident at once, a multiple of the groups, no more than the rows need
+template <typename K>
+cudaError_t blocks_for(K kern, int threads, const NormArgs &a, int rows, int *blocks) {
+    KernelSetup ks;
+    const cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), 0, threads, false, &ks);
+    if (e != cudaSuccess) return e;
+    long long per = (long long)ks.sms * ks.blocks_per_sm;
+    if (per > kMaxBlocks) per = kMaxBlocks;
+    per /= a.G;
     if (per < 1) per = 1;
-    if (per > need) per = need;
-    return (int)(per * G);
+    const long long need = (a.n + rows - 1) / rows;
+    *blocks = (int)((per < need ? per : need) * a.G);
+    return cudaSuccess;
 }
 
 template <typename T, int VEC, int LPR, int EPL>
 cudaError_t run(const NormArgs &a, bool back, cudaStream_t st) {
     using Sh = Shape<LPR>;
-    if (!back) {
-        const int blocks = blocks_for(a.n, a.G, Sh::ROWS, kMaxBlocks);
-        norm_kernel<T, VEC, LPR, EPL><<<blocks, Sh::NT, 0, st>>>(a);
-        return cudaGetLastError();
-    }
-    const int blocks = blocks_for(a.n, a.G, Sh::ROWS, kMaxBlocks);
-    norm_backward_kernel<T, VEC, LPR, EPL><<<blocks, Sh::NT, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.part) return e;
-    norm_params_kernel<<<dim3((a.d + 31) / 32, a.G), 256, 0, st>>>(a, blocks);
-    return cudaGetLastError();
+    int blocks = 0;
+    auto kern = back ? norm_backward_kernel<T, VEC, LPR, EPL> : norm_kernel<T, VEC, LPR, EPL>;
+    cudaError_t e = blocks_for(kern, Sh::NT, a, Sh::ROWS, &blocks);
+    if (e != cudaSuccess) return e;
+    kern<<<blocks, Sh::NT, 0, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !back || !a.part) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.d + 31) / 32, a.G);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_params_kernel, a, blocks);
 }
 
 template <typename T, int VEC>
 cudaError_t by_width(const NormArgs &a, bool back, cudaStream_t st) {
     if (a.d <= 64) return run<T, VEC, 8, 8>(a, back, st);
-    if (a.d <= 128) return run<T, VEC, 16, 8>(a, back, st);
-    if (a.d <= 256) return run<T, VEC, 32, 8>(a, back, st);
+    if (a.d <= 128) return run<T, VEC, 8, 16>(a, back, st);
+    if (a.d <= 256) return run<T, VEC, 16, 16>(a, back, st);
     if (a.d <= 512) return run<T, VEC, 32, 16>(a, back, st);
     if (a.d <= 1024) return run<T, VEC, 32, 32>(a, back, st);
     if (a.d <= 2048) return run<T, VEC, 256, 8>(a, back, st);
