@@ -5,9 +5,10 @@
 //
 // A row is held in the registers of LPR threads, EPL elements each, so x (and dy) is read once and
 // the variance is the mean of squared deviations from a mean that is already known.  LPR <= 32: a row
-// per part of a warp, sums by shuffles; LPR = 256 or 512: a row per CTA.  All sums are fp32.
+// per part of a warp, sums by shuffles; LPR >= 128: a row per CTA.  All sums are fp32.
 // Both directions are bound by HBM: the forward moves 2 d elements per row, the backward 3 d.  A row's
-// reductions are a chain of latencies, so the next row's loads are issued before them, and the launch has as
+// reductions are a chain of latencies, so the next row's loads are issued before them; its arithmetic is packed
+// (two fp32 per instruction: with one, issue bounds the kernels before HBM does); and the launch has as
 // many CTAs as are resident at once (a second, partial wave cost up to a third).
 //
 // dw and db: a row's threads always own the same columns of the same group, so each keeps its columns'
@@ -71,6 +72,8 @@ template <int LPR>
 struct Shape {
     static constexpr int NT = LPR <= 32 ? 256 : LPR;
     static constexpr int ROWS = NT / LPR;                // rows of a CTA at a time
+    // CTAs per SM that the registers must allow: 768 threads forwards, 512 backwards
+    static constexpr int FWD = NT >= 768 ? 1 : 768 / NT, BWD = NT >= 512 ? 1 : 512 / NT;
 };
 
 // N sums over the LPR threads of a row; every one of them gets them.  Over a CTA: one barrier, on two buffers in
@@ -112,7 +115,7 @@ struct Rows {
 
 // A CTA serves one group.
 template <typename T, int VEC, int LPR, int EPL>
-__global__ void __launch_bounds__(Shape<LPR>::NT) norm_kernel(NormArgs a)
+__global__ void __launch_bounds__(Shape<LPR>::NT, Shape<LPR>::FWD) norm_kernel(NormArgs a)
 {
     constexpr int NV = EPL / VEC;
     typedef typename Raw<T, VEC>::type raw_t;
@@ -121,15 +124,15 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_kernel(NormArgs a)
     const int g = blockIdx.x % a.G, lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
     const Rows<LPR> rows(a);
     const float width = (float)a.d, inv = 1.f / width;
-    float w[EPL], b[EPL];
+    f32x2 w[EPL / 2], b[EPL / 2];
+    auto param = [&](const float *p, int e, float other) {
+        const int c = (e / VEC * LPR + lane) * VEC + e % VEC;
+        return p && c < a.d ? __ldg(p + (size_t)g * a.d + c) : other;
+    };
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * LPR + lane) * VEC;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w[j * VEC + e] = a.weight && c < a.d ? __ldg(a.weight + (size_t)g * a.d + c + e) : 1.f;
-            b[j * VEC + e] = a.bias && c < a.d ? __ldg(a.bias + (size_t)g * a.d + c + e) : 0.f;
-        }
+    for (int e = 0; e < EPL; e += 2) {
+        w[e / 2] = pk2(param(a.weight, e, 1.f), param(a.weight, e + 1, 1.f));
+        b[e / 2] = pk2(param(a.bias, e, 0.f), param(a.bias, e + 1, 0.f));
     }
     raw_t next[NV] = {};
     auto fetch = [&](long long i0) {
@@ -143,26 +146,32 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_kernel(NormArgs a)
     fetch(rows.first);
     for (long long i0 = rows.first; i0 < a.n; i0 += rows.step) {
         const long long i = i0 + sub;
-        float v[EPL], s[1] = {0.f};
+        float v[EPL], s[1];
 #pragma unroll
         for (int j = 0; j < NV; ++j) widen<T, VEC>(v + j * VEC, next[j]);   // (zero behind the row's end)
         fetch(i0 + rows.step);
+        f32x2 x[EPL / 2], s2 = 0;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) s[0] += v[e];
+        for (int e = 0; e < EPL / 2; ++e) {
+            x[e] = pk2(v[2 * e], v[2 * e + 1]);
+            s2 = add2(s2, x[e]);
+        }
+        s[0] = x2(s2) + y2(s2);
         sum(s);
         const float mean = s[0] / width;      // (not a product with 1 / d: a constant row's mean is its value)
-        s[0] = 0.f;
+        const f32x2 mean2 = pk2(mean, mean);
+        s2 = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const bool in = (j * LPR + lane) * VEC < a.d;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                v[j * VEC + e] -= mean;
-                if (in) s[0] = fmaf(v[j * VEC + e], v[j * VEC + e], s[0]);
-            }
+        for (int e = 0; e < EPL / 2; ++e) {
+            x[e] = sub2(x[e], mean2);
+            const f32x2 in = pk2((2 * e / VEC * LPR + lane) * VEC < a.d ? x2(x[e]) : 0.f,
+                                 ((2 * e + 1) / VEC * LPR + lane) * VEC < a.d ? y2(x[e]) : 0.f);
+            s2 = fma2(in, in, s2);
         }
+        s[0] = x2(s2) + y2(s2);
         sum(s);
         const float rstd = rsqrtf(fmaf(s[0], inv, a.eps));
+        const f32x2 rstd2 = pk2(rstd, rstd);
         if (i >= a.n) continue;
         const size_t row = (size_t)i * a.G + g;
         T *y = static_cast<T *>(a.y) + row * a.d;
@@ -172,7 +181,11 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_kernel(NormArgs a)
             if (c >= a.d) continue;
             float o[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[j * VEC + e] * rstd, w[j * VEC + e], b[j * VEC + e]);
+            for (int e = 0; e < VEC; ++e) {
+                const int k = (j * VEC + e) / 2;
+                const f32x2 r = fma2(mul2(x[k], rstd2), w[k], b[k]);
+                o[e] = (j * VEC + e) % 2 ? y2(r) : x2(r);
+            }
             store_vec<T, VEC>(y + c, o);
         }
         if (lane == 0) {
@@ -183,7 +196,7 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_kernel(NormArgs a)
 }
 
 template <typename T, int VEC, int LPR, int EPL>
-__global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs a)
+__global__ void __launch_bounds__(Shape<LPR>::NT, Shape<LPR>::BWD) norm_backward_kernel(NormArgs a)
 {
     constexpr int ROWS = Shape<LPR>::ROWS, NV = EPL / VEC;
     typedef typename Raw<T, VEC>::type raw_t;
@@ -193,15 +206,15 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs 
     const int g = blockIdx.x % a.G, lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
     const Rows<LPR> rows(a);
     const float inv = 1.f / (float)a.d;
-    float w[EPL], dw[EPL], db[EPL];
+    f32x2 w[EPL / 2], dw[EPL / 2], db[EPL / 2];
+    auto param = [&](int e) {
+        const int c = (e / VEC * LPR + lane) * VEC + e % VEC;
+        return a.weight && c < a.d ? __ldg(a.weight + (size_t)g * a.d + c) : 1.f;
+    };
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * LPR + lane) * VEC;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w[j * VEC + e] = a.weight && c < a.d ? __ldg(a.weight + (size_t)g * a.d + c + e) : 1.f;
-            dw[j * VEC + e] = db[j * VEC + e] = 0.f;
-        }
+    for (int e = 0; e < EPL / 2; ++e) {
+        w[e] = pk2(param(2 * e), param(2 * e + 1));
+        dw[e] = db[e] = 0;
     }
     // a place without an element or a row holds zeros: dy's make every term of it vanish
     raw_t next_x[NV] = {}, next_dy[NV] = {};
@@ -218,10 +231,10 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs 
         const T *x = static_cast<const T *>(a.x) + row * a.d, *dy = static_cast<const T *>(a.dy) + row * a.d;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if ((j * LPR + lane) * VEC < a.d) {
-                next_x[j] = load_raw<T, VEC>(x + (j * LPR + lane) * VEC);
-                next_dy[j] = load_raw<T, VEC>(dy + (j * LPR + lane) * VEC);
-            }
+            const int c = (j * LPR + lane) * VEC;
+            if (c >= a.d) continue;
+            next_x[j] = load_raw<T, VEC>(x + c);
+            next_dy[j] = load_raw<T, VEC>(dy + c);
         }
         next_mean = __ldg(a.mean + row);
         next_rstd = __ldg(a.rstd + row);
@@ -229,26 +242,30 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs 
     fetch(rows.first);
     for (long long i0 = rows.first; i0 < a.n; i0 += rows.step) {
         const long long i = i0 + sub;
-        float xh[EPL], u[EPL], s[2] = {0.f, 0.f};
-        const float mean = next_mean, rstd = next_rstd;
+        float vx[EPL], vy[EPL], s[2];
+        const f32x2 mean2 = pk2(next_mean, next_mean), rstd2 = pk2(next_rstd, next_rstd);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            widen<T, VEC>(xh + j * VEC, next_x[j]);
-            widen<T, VEC>(u + j * VEC, next_dy[j]);
+            widen<T, VEC>(vx + j * VEC, next_x[j]);
+            widen<T, VEC>(vy + j * VEC, next_dy[j]);
         }
         fetch(i0 + rows.step);
+        f32x2 xh[EPL / 2], u[EPL / 2], s1 = 0, s2 = 0;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) {
-            xh[e] = (xh[e] - mean) * rstd;
-            dw[e] = fmaf(xh[e], u[e], dw[e]);
-            db[e] += u[e];
-            u[e] *= w[e];
-            s[0] += u[e];
-            s[1] = fmaf(u[e], xh[e], s[1]);
+        for (int e = 0; e < EPL / 2; ++e) {
+            xh[e] = mul2(sub2(pk2(vx[2 * e], vx[2 * e + 1]), mean2), rstd2);
+            u[e] = pk2(vy[2 * e], vy[2 * e + 1]);
+            dw[e] = fma2(xh[e], u[e], dw[e]);
+            db[e] = add2(db[e], u[e]);
+            u[e] = mul2(u[e], w[e]);
+            s1 = add2(s1, u[e]);
+            s2 = fma2(u[e], xh[e], s2);
         }
+        s[0] = x2(s1) + y2(s1);
+        s[1] = x2(s2) + y2(s2);
         sum(s);
         if (i >= a.n) continue;
-        const float m1 = s[0] * inv, m2 = s[1] * inv;
+        const f32x2 m1 = pk2(s[0] * inv, s[0] * inv), m2 = pk2(-s[1] * inv, -s[1] * inv);
         T *dx = static_cast<T *>(a.dx) + ((size_t)i * a.G + g) * a.d;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -256,13 +273,18 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs 
             if (c >= a.d) continue;
             float o[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = rstd * (u[j * VEC + e] - m1 - xh[j * VEC + e] * m2);
+            for (int e = 0; e < VEC; ++e) {
+                const int k = (j * VEC + e) / 2;
+                const f32x2 r = mul2(rstd2, fma2(xh[k], m2, sub2(u[k], m1)));
+                o[e] = (j * VEC + e) % 2 ? y2(r) : x2(r);
+            }
             store_vec<T, VEC>(dx + c, o);
         }
     }
     asm volatile("griddepcontrol.launch_dependents;");
     if (!a.part) return;
     // the CTA's share: [CTA][2][d]
+    auto value = [&](int which, int e) { const f32x2 p = which ? db[e / 2] : dw[e / 2]; return e % 2 ? y2(p) : x2(p); };
     float *part = a.part + (size_t)blockIdx.x * 2 * a.d;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
@@ -271,7 +293,7 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs 
             if constexpr (ROWS > 1) {
                 __syncthreads();
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) join[sub][lane * VEC + e] = which ? db[j * VEC + e] : dw[j * VEC + e];
+                for (int e = 0; e < VEC; ++e) join[sub][lane * VEC + e] = value(which, j * VEC + e);
                 __syncthreads();
                 for (int c = threadIdx.x; c < LPR * VEC; c += Shape<LPR>::NT) {
                     float s = 0.f;
@@ -283,7 +305,7 @@ __global__ void __launch_bounds__(Shape<LPR>::NT) norm_backward_kernel(NormArgs 
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const int c = (j * LPR + lane) * VEC + e;
-                    if (c < a.d) part[which * a.d + c] = which ? db[j * VEC + e] : dw[j * VEC + e];
+                    if (c < a.d) part[which * a.d + c] = value(which, j * VEC + e);
                 }
             }
         }
@@ -354,17 +376,20 @@ cudaError_t run(const NormArgs &a, bool back, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, norm_params_kernel, a, blocks);
 }
 
+// Within a warp 16 elements per thread (8 for the narrowest rows): against 8, a row of 128 costs a quarter fewer
+// instructions, which is what bounds short rows.  Across a CTA the rows in flight per SM count: the smallest CTA
+// whose backward (five values per element) still leaves room for a second one.
 template <typename T, int VEC>
 cudaError_t by_width(const NormArgs &a, bool back, cudaStream_t st) {
     if (a.d <= 64) return run<T, VEC, 8, 8>(a, back, st);
     if (a.d <= 128) return run<T, VEC, 8, 16>(a, back, st);
     if (a.d <= 256) return run<T, VEC, 16, 16>(a, back, st);
     if (a.d <= 512) return run<T, VEC, 32, 16>(a, back, st);
-    if (a.d <= 1024) return run<T, VEC, 32, 32>(a, back, st);
+    if (a.d <= 1024) return run<T, VEC, 128, 8>(a, back, st);
     if (a.d <= 2048) return run<T, VEC, 256, 8>(a, back, st);
     if (a.d <= 4096) return run<T, VEC, 256, 16>(a, back, st);
-    if (a.d <= 8192) return run<T, VEC, 256, 32>(a, back, st);
-    return run<T, VEC, 512, 32>(a, back, st);
+    if (a.d <= 8192) return run<T, VEC, 512, 16>(a, back, st);
+    return run<T, VEC, 1024, 16>(a, back, st);
 }
 cudaError_t launch(const NormArgs &a, bool bf16_in, bool back, cudaStream_t st) {
     if (bf16_in) return a.d % 8 == 0 ? by_width<bf16, 8>(a, back, st) : by_width<bf16, 1>(a, back, st);
