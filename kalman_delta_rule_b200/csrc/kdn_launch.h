@@ -71,11 +71,11 @@ size_t scan_tma_workspace_bytes(long long nchains, long long nchunks_max);
 cudaError_t launch_gain_scan_tma(const ScanArgs &a, long long ntok, void *workspace, cudaStream_t st);
 
 // ---- linear attention with a decay for each head
-// fp32 CUDA-core path in chunks of 64 tokens: chunk contributions, their scan, outputs / gradients
+// fp32 inputs (and problems without tokens, whatever their type), CUDA cores in chunks of 64 tokens
 size_t linear_simt_workspace_bytes(const LinArgs &a);
 size_t linear_simt_backward_workspace_bytes(const LinArgs &a);
-cudaError_t launch_linear_simt(const LinArgs &a, bool bf16_in, void *workspace, cudaStream_t st);
-cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, bool bf16_in, void *workspace, cudaStream_t st);
+cudaError_t launch_linear_simt(const LinArgs &a, void *workspace, cudaStream_t st);
+cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, void *workspace, cudaStream_t st);
 // tensor-core path in chunks of 128 tokens (bf16 inputs)
 size_t linear_tc_workspace_bytes(const LinArgs &a);
 cudaError_t launch_linear_tc(const LinArgs &a, void *workspace, cudaStream_t st);

@@ -92,7 +92,7 @@ kdn_status_t kdn_linear_forward(const kdn_linear_problem_t *p, const void *q, co
     a.err = kdn::error_word();
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (on_tensor_cores(p, a)) return cuda_status(kdn::launch_linear_tc(a, workspace, cs));
-    return cuda_status(kdn::launch_linear_simt(a, p->in_dtype == KDN_DTYPE_BF16, workspace, cs));
+    return cuda_status(kdn::launch_linear_simt(a, workspace, cs));
 }
 
 kdn_status_t kdn_linear_decode_tokens(int N, int n_tokens, int H, int d_k, int d_v, kdn_dtype_t in_dtype, float scale,
@@ -145,7 +145,7 @@ kdn_status_t kdn_linear_backward(const kdn_linear_problem_t *p, const void *q, c
     a.err = kdn::error_word();
     b.d_o = d_o; b.dS_T = dS_T; b.dq = dq; b.dk = dk; b.dv = dv; b.dg = dg; b.dS0 = dS0;
     if (on_tensor_cores(p, a)) return cuda_status(kdn::launch_linear_tc_backward(b, workspace, cs));
-    return cuda_status(kdn::launch_linear_simt_backward(b, p->in_dtype == KDN_DTYPE_BF16, workspace, cs));
+    return cuda_status(kdn::launch_linear_simt_backward(b, workspace, cs));
 }
 
 kdn_status_t kdn_layer_norm(long long n, int G, int d, kdn_dtype_t dtype, float eps, const void *x, const float *weight,

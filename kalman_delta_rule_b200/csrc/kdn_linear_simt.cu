@@ -1,4 +1,4 @@
-// Linear attention with a decay for each head on CUDA cores, fp32 arithmetic, in chunks of 64 tokens
+// Linear attention with a decay for each head for fp32 inputs: CUDA cores, in chunks of 64 tokens
 // (the recurrence unrolled as in kdn_linear.cuh).  Every step is parallel over chunks but one:
 //   delta  per (chunk, head, d_v tile): the chunk's own contribution U = K^T diag(w) V (w = decay to
 //          the chunk's end) or, for the gradient, E = scale Q^T diag(e^G) dO, and the chunk's decay
@@ -60,9 +60,9 @@ __device__ __forceinline__ void mm(float (&acc)[4][NJ], const float *A, int lda,
 
 // rows [0, L) of W columns from a token tensor ([ntok, H, d], column col) to shared memory [C][W + PAD];
 // rows behind the piece's end are zero, whatever the next sequence's rows hold
-template <int W, typename Tin>
+template <int W>
 __device__ __forceinline__ void load_rows(float *dst, const void *src, int tok, int L, int H, int h, int d, int col) {
-    const Tin *p = static_cast<const Tin *>(src) + ((size_t)tok * H + h) * d + col;
+    const float *p = static_cast<const float *>(src) + ((size_t)tok * H + h) * d + col;
     const size_t rs = (size_t)H * d;
     for (int i = threadIdx.x; i < C * (W / 4); i += NT) {
         const int r = i / (W / 4), c = (i % (W / 4)) * 4;
@@ -122,32 +122,46 @@ struct Ws {
 }  // namespace
 
 // ------------------------------------------------------------------ delta
-template <int DK, int DVT, typename Tin, bool REV>
-__global__ void __launch_bounds__(NT) linear_delta_kernel(LinArgs a, const void *X, const void *Y, float *out, float2 *dec)
+// What a launch of the first two steps works on; the backward's two directions are independent and share launches
+// (blockIdx.z): 0 forwards, 1 backwards.
+struct Walk {
+    const void *X, *Y;         // K, V;  Q, dO
+    float *U;                  // contributions, then states
+    const float *first;        // state before the first chunk;  gradient of the last state
+    float *last;               // state behind the last chunk;  gradient of the first state
+};
+struct Walks {
+    Walk w[2];
+};
+
+template <int DK, int DVT>
+__global__ void __launch_bounds__(NT) linear_delta_kernel(LinArgs a, Walks ws, float2 *dec)
 {
     extern __shared__ __align__(16) float sm[];
     float *Xs = sm, *Ys = sm + C * (DK + PAD);
     __shared__ ChunkDecay dec_s;
     const Log2 *G = dec_s.G;
+    const bool rev = blockIdx.z != 0;
+    const Walk &wk = ws.w[blockIdx.z];
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H, col = blockIdx.y * DVT;
     LinPiece p;
     if (!lin_piece(a, u, C, p) || p.len == 0) return;
     const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
-    load_rows<DK, Tin>(Xs, X, tok, L, a.H, h, DK, 0);
-    load_rows<DVT, Tin>(Ys, Y, tok, L, a.H, h, a.dv, col);
+    load_rows<DK>(Xs, wk.X, tok, L, a.H, h, DK, 0);
+    load_rows<DVT>(Ys, wk.Y, tok, L, a.H, h, a.dv, col);
     chunk_log_decay(a, tok, L, h, &dec_s);
     for (int i = threadIdx.x; i < L * (DVT / 4); i += NT) {
         const int r = i / (DVT / 4);
         float4 *y = reinterpret_cast<float4 *>(Ys + r * (DVT + PAD) + (i % (DVT / 4)) * 4);
-        *y = scale4(*y, dec_s.one * (REV ? a.scale * lin_exp2(G[r]) : lin_exp2_between(G[C - 1], G[r])));
+        *y = scale4(*y, dec_s.one * (rev ? a.scale * lin_exp2(G[r]) : lin_exp2_between(G[C - 1], G[r])));
     }
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
+    if (!rev && blockIdx.y == 0 && threadIdx.x == 0) {
         const float2 f = lin_chunk_decay(G[C - 1]);
         dec[(size_t)u * a.H + h] = make_float2(f.x * dec_s.one, f.y);
     }
     __syncthreads();
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float *dst = out + ((size_t)u * a.H + h) * DK * a.dv + col;
+    float *dst = wk.U + ((size_t)u * a.H + h) * DK * a.dv + col;
 #pragma unroll
     for (int m0 = 0; m0 < DK; m0 += 64) {
         if (ty * 4 >= DK) break;
@@ -163,9 +177,10 @@ __global__ void __launch_bounds__(NT) linear_delta_kernel(LinArgs a, const void 
 // ------------------------------------------------------------------ scan
 // thread = four elements of one (sequence, head)'s state; the chunks' contributions are fetched
 // eight at a time, so that the loads of a group overlap and only its multiply-adds are serial
-template <bool REV>
-__global__ void __launch_bounds__(256) linear_scan_kernel(LinArgs a, float *U, const float2 *dec, const float *first, float *last)
+__global__ void __launch_bounds__(256) linear_scan_kernel(LinArgs a, Walks ws, const float2 *dec)
 {
+    const bool rev = blockIdx.z != 0;
+    const Walk &wk = ws.w[blockIdx.z];
     const int per = a.dk * a.dv / 4;
     const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
     const int sh = (int)(id / per), e = (int)(id % per) * 4;
@@ -175,10 +190,10 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(LinArgs a, float *U, c
     lin_seq(a, s, t0, len);
     const int n = (len + C - 1) / C;
     const size_t st = (size_t)a.H * a.dk * a.dv;
-    float *p = U + ((size_t)lin_first_slot(a, s, t0, C) * a.H + h) * a.dk * a.dv + e;
+    float *p = wk.U + ((size_t)lin_first_slot(a, s, t0, C) * a.H + h) * a.dk * a.dv + e;
     const float2 *d = dec + (size_t)lin_first_slot(a, s, t0, C) * a.H + h;
     const size_t se = (size_t)sh * a.dk * a.dv + e;
-    float4 x = first ? *reinterpret_cast<const float4 *>(first + se) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 x = wk.first ? *reinterpret_cast<const float4 *>(wk.first + se) : make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int B = 8;
     for (int c0 = 0; c0 < n; c0 += B) {
         float4 y[B];
@@ -186,7 +201,7 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(LinArgs a, float *U, c
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             if (c0 + i < n) {
-                const int c = REV ? n - 1 - c0 - i : c0 + i;
+                const int c = rev ? n - 1 - c0 - i : c0 + i;
                 y[i] = *reinterpret_cast<const float4 *>(p + c * st);
                 f[i] = d[(size_t)c * a.H];
             }
@@ -194,18 +209,18 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(LinArgs a, float *U, c
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             if (c0 + i < n) {
-                const int c = REV ? n - 1 - c0 - i : c0 + i;
+                const int c = rev ? n - 1 - c0 - i : c0 + i;
                 *reinterpret_cast<float4 *>(p + c * st) = x;
                 x = make_float4(lin_carry(f[i], x.x, y[i].x), lin_carry(f[i], x.y, y[i].y), lin_carry(f[i], x.z, y[i].z),
                                 lin_carry(f[i], x.w, y[i].w));
             }
         }
     }
-    if (last) *reinterpret_cast<float4 *>(last + se) = x;
+    if (wk.last) *reinterpret_cast<float4 *>(wk.last + se) = x;
 }
 
 // ------------------------------------------------------------------ out
-template <int DK, int DVT, typename Tin>
+template <int DK, int DVT>
 __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *S)
 {
     extern __shared__ __align__(16) float sm[];
@@ -217,9 +232,9 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
     LinPiece p;
     if (!lin_piece(a, u, C, p) || p.len == 0) return;
     const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
-    load_rows<DK, Tin>(Qs, a.q, tok, L, a.H, h, DK, 0);
-    load_rows<DK, Tin>(Ks, a.k, tok, L, a.H, h, DK, 0);
-    load_rows<DVT, Tin>(Vs, a.v, tok, L, a.H, h, a.dv, col);
+    load_rows<DK>(Qs, a.q, tok, L, a.H, h, DK, 0);
+    load_rows<DK>(Ks, a.k, tok, L, a.H, h, DK, 0);
+    load_rows<DVT>(Vs, a.v, tok, L, a.H, h, a.dv, col);
     load_state<DK, DVT>(Ss, S + ((size_t)u * a.H + h) * DK * a.dv + col, a.dv);
     chunk_log_decay(a, tok, L, h, &dec_s);
     const float scale = a.scale * dec_s.one;
@@ -245,7 +260,7 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
         for (int j = 0; j < DVT / 16; ++j) acc[i][j] *= f;
     }
     mm<DVT / 16, false, false>(acc, Ps, C + PAD, Vs, DVT + PAD, C, ty, tx);
-    Tin *o = static_cast<Tin *>(a.o) + ((size_t)tok * a.H + h) * a.dv + col;
+    float *o = static_cast<float *>(a.o) + ((size_t)tok * a.H + h) * a.dv + col;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = ty * 4 + i;
@@ -262,14 +277,15 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
 //   dg_t = sum over pairs (query i >= t, key j < t), in the chunk, before and behind it:
 //        sum_{s >= t} (rows Z - columns Z)_s + sum_{s >= t} q_s.(a dO S^T)_s + sum_{s < t} k_s.(w V R^T)_s + e^{G_C} <S, R>
 // No term is divided by a decay, and none of the four cancels against another.
-template <int DK, int DVT, typename Tin>
-__global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
+template <int DK, int DVT>
+__global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
 {
     const LinArgs &a = b.a;
     constexpr int NK = DK / 16, NV = DVT / 16;
     extern __shared__ __align__(16) float sm[];
     float *Qs = sm, *Ks = Qs + C * (DK + PAD), *Vs = Ks + C * (DK + PAD), *Os = Vs + C * (DVT + PAD),
-          *Ss = Os + C * (DVT + PAD), *Rs = Ss + DK * (DVT + PAD), *Ps = Rs + DK * (DVT + PAD), *As = Ps + C * (C + PAD);
+          *Ss = Os + C * (DVT + PAD), *Ps = Ss + DK * (DVT + PAD);
+    float *const Rs = Ss, *const As = Ps;   // each takes the other's place once that has been read
     __shared__ ChunkDecay dec_s;
     const Log2 *G = dec_s.G;
     __shared__ float zr[C], zc[8][C], xi[C], yi[C], wsum[8];
@@ -279,8 +295,8 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
     const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const size_t sbase = ((size_t)u * a.H + h) * DK * a.dv;
-    load_rows<DK, Tin>(Qs, a.q, tok, L, a.H, h, DK, 0);
-    load_rows<DK, Tin>(Ks, a.k, tok, L, a.H, h, DK, 0);
+    load_rows<DK>(Qs, a.q, tok, L, a.H, h, DK, 0);
+    load_rows<DK>(Ks, a.k, tok, L, a.H, h, DK, 0);
     chunk_log_decay(a, tok, L, h, &dec_s);
 
     const float scale = a.scale * dec_s.one;
@@ -299,17 +315,21 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
     float sr = 0.f;
     for (int col = 0; col < a.dv; col += DVT) {
         __syncthreads();       // the previous tile is read; Ps is written
-        load_rows<DVT, Tin>(Vs, a.v, tok, L, a.H, h, a.dv, col);
-        load_rows<DVT, Tin>(Os, b.d_o, tok, L, a.H, h, a.dv, col);
+        load_rows<DVT>(Vs, a.v, tok, L, a.H, h, a.dv, col);
+        load_rows<DVT>(Os, b.d_o, tok, L, a.H, h, a.dv, col);
         load_state<DK, DVT>(Ss, ws.U + sbase + col, a.dv);
-        load_state<DK, DVT>(Rs, ws.E + sbase + col, a.dv);
         __syncthreads();
-        for (int i = threadIdx.x; i < DK * DVT; i += NT) {
-            const int e = (i / DVT) * (DVT + PAD) + i % DVT;
-            sr = fmaf(Ss[e], Rs[e], sr);
-        }
         mm<4, false, true>(dp, Os, DVT + PAD, Vs, DVT + PAD, DVT, ty, tx);
         mm<NK, false, true>(dqi, Os, DVT + PAD, Ss, DVT + PAD, DVT, ty, tx);
+        __syncthreads();
+        for (int i = threadIdx.x; i < DK * (DVT / 4); i += NT) {   // R over S, and their inner product
+            const int r = i / (DVT / 4), c = (i % (DVT / 4)) * 4;
+            float4 *at = reinterpret_cast<float4 *>(Ss + r * (DVT + PAD) + c);
+            const float4 x = *at, y = *reinterpret_cast<const float4 *>(ws.E + sbase + col + (size_t)r * a.dv + c);
+            sr = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, sr))));
+            *at = y;
+        }
+        __syncthreads();
         mm<NK, false, true>(dki, Vs, DVT + PAD, Rs, DVT + PAD, DVT, ty, tx);
         float acc[4][NV] = {};
         mm<NV, false, false>(acc, Ks, DK + PAD, Rs, DVT + PAD, DK, ty, tx);
@@ -320,7 +340,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
             for (int j = 0; j < NV; ++j) acc[i][j] *= w;
         }
         mm<NV, true, false>(acc, Ps, C + PAD, Os, DVT + PAD, C, ty, tx);
-        Tin *dv = static_cast<Tin *>(b.dv) + ((size_t)tok * a.H + h) * a.dv + col;
+        float *dv = static_cast<float *>(b.dv) + ((size_t)tok * a.H + h) * a.dv + col;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = ty * 4 + i;
@@ -331,6 +351,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
     }
 
     // ---- dA to shared memory; rows and columns of Z; the boundary terms of the decay's gradient
+    __syncthreads();           // P has been read
     float zcol[4] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -369,7 +390,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
 
     mm<NK, false, false>(dqi, As, C + PAD, Ks, DK + PAD, C, ty, tx);
     mm<NK, true, false>(dki, As, C + PAD, Qs, DK + PAD, C, ty, tx);
-    Tin *dq = static_cast<Tin *>(b.dq) + ((size_t)tok * a.H + h) * DK, *dk = static_cast<Tin *>(b.dk) + ((size_t)tok * a.H + h) * DK;
+    float *dq = static_cast<float *>(b.dq) + ((size_t)tok * a.H + h) * DK, *dk = static_cast<float *>(b.dk) + ((size_t)tok * a.H + h) * DK;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = ty * 4 + i;
@@ -447,41 +468,38 @@ long long slots_of(const LinArgs &a) { return lin_slots(a.cu != nullptr, a.T, a.
 size_t state_bytes(const LinArgs &a) { return round256((size_t)slots_of(a) * a.H * a.dk * a.dv * 4); }
 size_t head_bytes(const LinArgs &a) { return round256((size_t)slots_of(a) * a.H * 8); }
 
-template <int DK, int DVT, typename Tin, bool REV>
-cudaError_t delta(const LinArgs &a, const void *X, const void *Y, float *out, float2 *dec, cudaStream_t st) {
+// the first two steps for one direction or both
+template <int DK, int DVT>
+cudaError_t states(const LinArgs &a, const Walks &ws, int walks, float2 *dec, cudaStream_t st) {
     constexpr size_t smem = sizeof(float) * C * (DK + DVT + 2 * PAD);
     KernelSetup ks;
-    auto kern = linear_delta_kernel<DK, DVT, Tin, REV>;
+    auto kern = linear_delta_kernel<DK, DVT>;
     cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT), NT, smem, st>>>(a, X, Y, out, dec);
-    return cudaGetLastError();
-}
-template <bool REV>
-cudaError_t scan(const LinArgs &a, float *U, const float2 *dec, const float *first, float *last, cudaStream_t st) {
+    kern<<<dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT, walks), NT, smem, st>>>(a, ws, dec);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     const long long threads = (long long)a.nseq * a.H * (a.dk * a.dv / 4);
-    linear_scan_kernel<REV><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, U, dec, first, last);
+    linear_scan_kernel<<<dim3((unsigned)((threads + 255) / 256), 1, walks), 256, 0, st>>>(a, ws, dec);
     return cudaGetLastError();
 }
 
-template <int DK, int DVT, typename Tin>
+template <int DK, int DVT>
 cudaError_t forward(const LinArgs &a, uint8_t *ws, cudaStream_t st) {
     float *U = reinterpret_cast<float *>(ws);
-    float2 *dec = reinterpret_cast<float2 *>(ws + state_bytes(a));
-    cudaError_t e = delta<DK, DVT, Tin, false>(a, a.k, a.v, U, dec, st);
-    if (e != cudaSuccess) return e;
-    e = scan<false>(a, U, dec, a.S0, a.S_out, st);
+    const Walks wk{{{a.k, a.v, U, a.S0, a.S_out}, {}}};
+    cudaError_t e = states<DK, DVT>(a, wk, 1, reinterpret_cast<float2 *>(ws + state_bytes(a)), st);
     if (e != cudaSuccess) return e;
     constexpr size_t smem = sizeof(float) * (C * (2 * DK + DVT + C + 4 * PAD) + DK * (DVT + PAD));
     KernelSetup ks;
-    auto kern = linear_out_kernel<DK, DVT, Tin>;
+    auto kern = linear_out_kernel<DK, DVT>;
     e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
     if (e != cudaSuccess) return e;
     kern<<<dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT), NT, smem, st>>>(a, U);
     return cudaGetLastError();
 }
 
-template <int DK, int DVT, typename Tin>
+template <int DK, int DVT>
 cudaError_t backward(const LinBwdArgs &b, uint8_t *wsp, cudaStream_t st) {
     const LinArgs &a = b.a;
     Ws ws;
@@ -489,14 +507,12 @@ cudaError_t backward(const LinBwdArgs &b, uint8_t *wsp, cudaStream_t st) {
     ws.E = reinterpret_cast<float *>(wsp + state_bytes(a));
     ws.dec = reinterpret_cast<float2 *>(wsp + 2 * state_bytes(a));
     ws.dgc = reinterpret_cast<float *>(wsp + 2 * state_bytes(a) + head_bytes(a));
-    cudaError_t e = delta<DK, DVT, Tin, false>(a, a.k, a.v, ws.U, ws.dec, st);
-    if (e == cudaSuccess) e = scan<false>(a, ws.U, ws.dec, a.S0, nullptr, st);
-    if (e == cudaSuccess) e = delta<DK, DVT, Tin, true>(a, a.q, b.d_o, ws.E, ws.dec, st);
-    if (e == cudaSuccess) e = scan<true>(a, ws.E, ws.dec, b.dS_T, b.dS0, st);
+    const Walks wk{{{a.k, a.v, ws.U, a.S0, nullptr}, {a.q, b.d_o, ws.E, b.dS_T, b.dS0}}};
+    cudaError_t e = states<DK, DVT>(a, wk, 2, ws.dec, st);
     if (e != cudaSuccess) return e;
-    constexpr size_t smem = sizeof(float) * (C * (2 * DK + 2 * DVT + 2 * C + 6 * PAD) + 2 * DK * (DVT + PAD));
+    constexpr size_t smem = sizeof(float) * (C * (2 * DK + 2 * DVT + C + 5 * PAD) + DK * (DVT + PAD));
     KernelSetup ks;
-    auto kern = linear_grad_kernel<DK, DVT, Tin>;
+    auto kern = linear_grad_kernel<DK, DVT>;
     e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(slots_of(a) * a.H), NT, smem, st>>>(b, ws);
@@ -505,26 +521,24 @@ cudaError_t backward(const LinBwdArgs &b, uint8_t *wsp, cudaStream_t st) {
     return launch_linear_head_decay(a, ws.dgc, b.dg, C, st);
 }
 
-#define KDN_LINEAR_SIZES(FN, ARG)                                                                              \
-    if (a.dv == 32) {                                                                                          \
-        if (a.dk == 32) return bf16_in ? FN<32, 32, bf16>(ARG, w, st) : FN<32, 32, float>(ARG, w, st);         \
-        if (a.dk == 64) return bf16_in ? FN<64, 32, bf16>(ARG, w, st) : FN<64, 32, float>(ARG, w, st);         \
-        return bf16_in ? FN<128, 32, bf16>(ARG, w, st) : FN<128, 32, float>(ARG, w, st);                       \
-    }                                                                                                          \
-    if (a.dk == 32) return bf16_in ? FN<32, 64, bf16>(ARG, w, st) : FN<32, 64, float>(ARG, w, st);             \
-    if (a.dk == 64) return bf16_in ? FN<64, 64, bf16>(ARG, w, st) : FN<64, 64, float>(ARG, w, st);             \
-    return bf16_in ? FN<128, 64, bf16>(ARG, w, st) : FN<128, 64, float>(ARG, w, st);
+#define KDN_LINEAR_SIZES(FN, ARG)                                          \
+    if (a.dv == 32) {                                                      \
+        if (a.dk == 32) return FN<32, 32>(ARG, w, st);                     \
+        return a.dk == 64 ? FN<64, 32>(ARG, w, st) : FN<128, 32>(ARG, w, st); \
+    }                                                                      \
+    if (a.dk == 32) return FN<32, 64>(ARG, w, st);                         \
+    return a.dk == 64 ? FN<64, 64>(ARG, w, st) : FN<128, 64>(ARG, w, st);
 
 }  // namespace
 
 size_t linear_simt_workspace_bytes(const LinArgs &a) { return state_bytes(a) + head_bytes(a); }
 size_t linear_simt_backward_workspace_bytes(const LinArgs &a) { return 2 * state_bytes(a) + 2 * head_bytes(a); }
 
-cudaError_t launch_linear_simt(const LinArgs &a, bool bf16_in, void *workspace, cudaStream_t st) {
+cudaError_t launch_linear_simt(const LinArgs &a, void *workspace, cudaStream_t st) {
     uint8_t *w = static_cast<uint8_t *>(workspace);
     KDN_LINEAR_SIZES(forward, a)
 }
-cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, bool bf16_in, void *workspace, cudaStream_t st) {
+cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, void *workspace, cudaStream_t st) {
     const LinArgs &a = b.a;
     uint8_t *w = static_cast<uint8_t *>(workspace);
     KDN_LINEAR_SIZES(backward, b)
