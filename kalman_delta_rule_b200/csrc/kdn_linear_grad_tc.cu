@@ -77,6 +77,9 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     const Decay &d = *reinterpret_cast<const Decay *>(sm + L_::DEC);
     float *zr = reinterpret_cast<float *>(sm + L_::SUM), *zc = zr + 4 * C, *xi = zc + 4 * C, *yi = xi + 4 * C, *sr_w = yi + 4 * C;
 
+    auto load = [&](const CUtensorMap *m, int region, int c0, int n) {   // (thread 0)
+        for (int t = 0; t < n; ++t) load_tile(sm + region + t * ATOM, m, c0 + t * 64, h, tok, bar_tma);
+    };
     if (threadIdx.x == 0) {
         mbar_init(bar_tma, 1);
         mbar_init(bar_a, 1);
@@ -84,7 +87,22 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
         mbar_init(bar_c, 1);
         mbar_fence_init();
         *abort_flag = (sb & 1023u) ? 1 : 0;
+        mbar_expect_tx(bar_tma, (uint32_t)(2 * KATOMS + 2 * nt) * ATOM + (uint32_t)sizeof(Decay));
+        bulk_load(sm + L_::DEC, f.s.decay + (size_t)u * a.H + h, sizeof(Decay), bar_tma);
+        load(&f.tq, L_::Q, 0, KATOMS);
+        load(&f.tk, L_::K, 0, KATOMS);
+        load(&f.to, L_::DO, 0, nt);
+        load(&f.tv, L_::V, 0, nt);
     }
+    // 16 columns of a state tile's row in registers
+    auto fetch = [&](const float *base, int t, float4 (&x)[4]) {
+        const float *tile = base + tile_at(u, a.H, h, tiles, t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __ldg(reinterpret_cast<const float4 *>(tile + ((cg * 4 + j) * 128 + row) * 4));
+    };
+    float4 S[4], R[4];
+    fetch(f.s.S, 0, S);
+    fetch(f.s.R, 0, R);
     if (warp == 0) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
@@ -102,15 +120,7 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
         __syncthreads();
         tc_fence_after();
     };
-    auto load = [&](const CUtensorMap *m, int region, int c0, int n) {   // (thread 0)
-        for (int t = 0; t < n; ++t) load_tile(sm + region + t * ATOM, m, c0 + t * 64, h, tok, bar_tma);
-    };
-    // 16 columns of a state tile's row in registers, and as terms in shared memory
-    auto fetch = [&](const float *base, int t, float4 (&x)[4]) {
-        const float *tile = base + tile_at(u, a.H, h, tiles, t);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = __ldg(reinterpret_cast<const float4 *>(tile + ((cg * 4 + j) * 128 + row) * 4));
-    };
+    // 16 columns of a state tile's row, as terms in shared memory
     auto terms = [&](const float4 (&x)[4], int p0, int p1, int p2) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -133,20 +143,9 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             for (int t = 0; t < n; ++t) zero_row(sm + tile + t * ATOM, row, cg * 2, 2);
     };
 
-    if (threadIdx.x == 0) {
-        mbar_expect_tx(bar_tma, (uint32_t)(2 * KATOMS + 2 * nt) * ATOM + (uint32_t)sizeof(Decay));
-        bulk_load(sm + L_::DEC, f.s.decay + (size_t)u * a.H + h, sizeof(Decay), bar_tma);
-        load(&f.tq, L_::Q, 0, KATOMS);
-        load(&f.tk, L_::K, 0, KATOMS);
-        load(&f.to, L_::DO, 0, nt);
-        load(&f.tv, L_::V, 0, nt);
-    }
     // ---- products with the states, tile after tile of d_v (two are resident); the scores with the first.  The terms of
     // the next operand are formed while the products of the one before run: S's in ST, R's in R1 and where q was
     float sr = 0.f;
-    float4 S[4], R[4];
-    fetch(f.s.S, 0, S);
-    fetch(f.s.R, 0, R);
     for (int t = 0; t < tiles; ++t) {
         const int i = t & 1;
         if (i == 0) {
@@ -282,8 +281,21 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     }
     wait_tma();
     zero_tail(L_::Q, KATOMS);
-    if (L < C) __syncthreads();               // (a row's channels are read by other threads than cleared them)
-    // ---- the states' parts of dQ and dK: dot products with q and k, rows scaled in place
+    // ---- dV's parts for the resident (last) half of d_v
+    const int last = (tiles - 1) & ~1;
+    auto value_parts = [&]() {                // P^T dO into the scores' columns, K R into dP's
+        if (nt == 2) {
+            mma_tiles<8, true, true, 128>(T_SC, sb + L_::P, sb + L_::DO, false);
+            mma_tiles<4 * KATOMS, false, true, 128>(T_DP, sb + L_::K, sb + L_::R1, false);
+        } else {
+            mma_tiles<8, true, true, 64>(T_SC, sb + L_::P, sb + L_::DO, false);
+            mma_tiles<4 * KATOMS, false, true, 64>(T_DP, sb + L_::K, sb + L_::R1, false);
+        }
+        mma_commit(bar_a);
+    };
+    publish();
+    if (warp == 0 && elect_one()) value_parts();
+    // ---- meanwhile the states' parts of dQ and dK: dot products with q and k, rows scaled in place
     if (cg < 2 * KATOMS) {
         const float fa = a.scale * since, fw = until;
         float xs = 0.f, ys = 0.f;
@@ -320,76 +332,53 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
     if (lane == 0) sr_w[warp] = sr;
     publish();
 
-    // ---- the rest of the products: dV's parts for the resident (last) half of d_v, dQ, dK
-    const int last = (tiles - 1) & ~1;
-    auto value_parts = [&]() {                // P^T dO into the scores' columns, K R into dP's
-        if (nt == 2) {
-            mma_tiles<8, true, true, 128>(T_SC, sb + L_::P, sb + L_::DO, false);
-            mma_tiles<4 * KATOMS, false, true, 128>(T_DP, sb + L_::K, sb + L_::R1, false);
-        } else {
-            mma_tiles<8, true, true, 64>(T_SC, sb + L_::P, sb + L_::DO, false);
-            mma_tiles<4 * KATOMS, false, true, 64>(T_DP, sb + L_::K, sb + L_::R1, false);
-        }
-        mma_commit(bar_a);
-    };
+    // ---- dQ, dK
     if (warp == 0 && elect_one()) {
-        value_parts();
         mma_tiles<8, false, true, NK>(T_DQ, sb + L_::DA, sb + L_::K, true);
         mma_commit(bar_b);
         mma_tiles<8, true, true, NK>(T_DK, sb + L_::DA, sb + L_::Q, true);
         mma_commit(bar_c);                    // (a barrier of its own: it must not run a phase ahead of a waiter)
     }
-    // meanwhile one warp sums up the decay's gradient, four tokens per lane
-    if (f.b.dg && warp == 1) {
-        float s0 = 0.f;
-#pragma unroll 1
-        for (int i = 0; i < NT / 32; ++i) s0 += sr_w[i];
-        const float whole = d.whole.x * s0;
-        Log2 later[4], earlier[4];            // sums in two floats, as for the decays
+    // meanwhile four warps sum up the decay's gradient, a token per thread: sums over the tokens from t on and before t
+    if (f.b.dg && warp < 4) {
+        const int t = threadIdx.x;
+        float later = 0.f, earlier = 0.f, s0 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int t = lane * 4 + e;
-            float rows = 0.f, cols = 0.f, x = 0.f, y = 0.f;
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                rows += zr[i * C + t];
-                cols += zc[i * C + t];
-                if (i < 2 * KATOMS) {
-                    x += xi[i * C + t];
-                    y += yi[i * C + t];
-                }
-            }
-            later[e] = Log2{rows, x} + Log2{-cols, 0.f};
-            earlier[e] = {y, 0.f};
+        for (int i = 0; i < 4; ++i) later += zr[i * C + t] - zc[i * C + t];
+#pragma unroll
+        for (int i = 0; i < 2 * KATOMS; ++i) {
+            later += xi[i * C + t];
+            earlier += yi[i * C + t];
         }
-        Log2 sl = (later[0] + later[1]) + (later[2] + later[3]), se = (earlier[0] + earlier[1]) + (earlier[2] + earlier[3]);
-        Log2 fl = sl, fe = se;
-#pragma unroll 1
+#pragma unroll
+        for (int i = 0; i < NT / 32; i += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(sr_w + i);
+            s0 += (x.x + x.y) + (x.z + x.w);
+        }
+        const float own = earlier;
+#pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const Log2 yl = {__shfl_down_sync(0xffffffffu, fl.hi, off), __shfl_down_sync(0xffffffffu, fl.lo, off)};
-            const Log2 ye = {__shfl_up_sync(0xffffffffu, fe.hi, off), __shfl_up_sync(0xffffffffu, fe.lo, off)};
-            if (lane + off < 32) fl = fl + yl;
-            if (lane >= off) fe = fe + ye;
+            const float yl = __shfl_down_sync(0xffffffffu, later, off), ye = __shfl_up_sync(0xffffffffu, earlier, off);
+            if (lane + off < 32) later += yl;
+            if (lane >= off) earlier += ye;
         }
-        Log2 after = fl - sl, before = fe - se;   // the lanes' above, below
-        float g[4];
-        for (int e = 3; e >= 0; --e) {
-            after = after + later[e];
-            g[e] = after.hi;
+        if (lane == 0) sr_w[16 + warp] = later;          // the warp's sums
+        if (lane == 31) sr_w[20 + warp] = earlier;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        earlier -= own;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i > warp) later += sr_w[16 + i];
+            if (i < warp) earlier += sr_w[20 + i];
         }
-        float sum = 0.f;
-        for (int e = 0; e < 4; ++e) {
-            g[e] = (g[e] + before.hi) + whole;
-            before = before + earlier[e];
-            const int t = lane * 4 + e;
-            if (t < L) {
-                sum += g[e];
-                if (a.decay == KDN_DECAY_TOKEN) f.b.dg[(size_t)(tok + t) * a.H + h] = g[e];
-            }
-        }
-        if (a.decay == KDN_DECAY_HEAD) {
-            sum = warp_sum(sum);
-            if (lane == 0) f.s.share[(size_t)u * a.H + h] = sum;
+        const float g = (later + earlier) + d.whole.x * s0;
+        if (a.decay == KDN_DECAY_TOKEN) {
+            if (t < L) f.b.dg[(size_t)(tok + t) * a.H + h] = g;
+        } else {
+            const float sum = warp_sum(t < L ? g : 0.f);
+            if (lane == 0) sr_w[24 + warp] = sum;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (t == 0) f.s.share[(size_t)u * a.H + h] = (sr_w[24] + sr_w[25]) + (sr_w[26] + sr_w[27]);
         }
     }
 
