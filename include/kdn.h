@@ -246,7 +246,8 @@ kdn_status_t kdn_backward(const kdn_problem_t *p,
  *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t        (readout after the write)
  *
  * Layouts, types, sizes, packed sequences, streams, errors and ownership are those of the head of
- * this file; the log decay is always fp32.  Tokens behind the last packed sequence are neither read
+ * this file; the log decay is always fp32; no output may alias an input (the state of the recurrent
+ * form apart) or another output.  Tokens behind the last packed sequence are neither read
  * nor written.  A sequence never sees another one's rows, whatever they hold; within a sequence a
  * non-finite input may also reach the outputs of the tokens shortly before it (those of its chunk,
  * up to 127 tokens). */
@@ -271,8 +272,7 @@ kdn_status_t kdn_linear_workspace_size(const kdn_linear_problem_t *p, size_t *by
 /* Forward over whole sequences (prompts, training), chunkwise.
  *  q, k      : device [B, T, H, d_k];  v, o : device [B, T, H, d_v]     (in_dtype)
  *  g         : device fp32, shape by `decay`
- *  S0        : device fp32 [N, H, d_k, d_v] or NULL (zero);  S_out : the same, final states, or NULL;
- *              they may not alias
+ *  S0        : device fp32 [N, H, d_k, d_v] or NULL (zero);  S_out : the same, final states, or NULL
  *  workspace : device, >= kdn_linear_workspace_size() bytes, 256-byte aligned (contents on entry do
  *              not matter; distinct per concurrent call).  Every other pointer 16-byte aligned. */
 kdn_status_t kdn_linear_forward(const kdn_linear_problem_t *p, const void *q, const void *k, const void *v,
@@ -296,7 +296,7 @@ kdn_status_t kdn_linear_decode_tokens(int N, int n_tokens, int H, int d_k, int d
  *               that the projections' gradients read
  *  dg         : device fp32, shape of g, or NULL (not written; must be NULL without a decay).  No
  *               gradient is divided by a decay, so g = -infinity is fine (its gradient is 0).
- *  dS0        : device fp32 [N, H, d_k, d_v] or NULL (not written); may not alias dS_T
+ *  dS0        : device fp32 [N, H, d_k, d_v] or NULL (not written)
  *  workspace  : as for the forward, of kdn_linear_backward_workspace_size() bytes.
  * Deterministic: no sum depends on the order in which blocks run. */
 kdn_status_t kdn_linear_backward_workspace_size(const kdn_linear_problem_t *p, size_t *bytes);
@@ -312,7 +312,7 @@ kdn_status_t kdn_linear_backward(const kdn_linear_problem_t *p, const void *q, c
  *     m = mean(x),  r = (mean((x - m)^2) + eps)^(-1/2),  y = (x - m) r * weight + bias
  *  x, y         : device [n, G, d] (dtype);  weight, bias : device fp32 [G, d], or NULL (1, 0)
  *  mean, rstd   : device fp32 [n, G], m and r for the backward, or NULL (not written)
- * 1 <= d <= 16384, G <= 65535, eps >= 0; every pointer 16-byte aligned. */
+ * 1 <= d <= 16384, G <= 65535, eps >= 0; every pointer 16-byte aligned; no output may alias an input. */
 kdn_status_t kdn_layer_norm(long long n, int G, int d, kdn_dtype_t dtype, float eps, const void *x,
                             const float *weight, const float *bias, void *y, float *mean, float *rstd, void *stream);
 

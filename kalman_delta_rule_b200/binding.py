@@ -602,7 +602,9 @@ def _norm_rows(x, weight):
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, y=None, stream=None):
     """Layer norm over the last axis (kdn_layer_norm); returns (y, mean, rstd), mean and rstd fp32 of
-    x.shape[:-1].  weight, bias: fp32 [d], or [G, d] for x [..., G, d] (a row for each head), or None."""
+    x.shape[:-1].  weight, bias: fp32 [d], or [G, d] for x [..., G, d] (a row for each head), or None.
+    (``layer_norm_backward`` returns the bias's gradient beside the weight's: a norm that trains a bias alone has
+    a weight of ones.)"""
     torch = _mod or _cuda()
     code = _type_of(torch, "x", x)
     dev = _device_of("x", x)
@@ -662,6 +664,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, workspace=None, stream=None):
             key = ("norm", n, G, d)
             need = _sizes.get(key)
             if need is None:
+                if len(_sizes) > 4096:
+                    _sizes.clear()
                 need = _sizes[key] = kdn_layer_norm_backward_workspace_size(n, G, d)
             ws, sp, sb = _work(torch, "layer_norm_backward", workspace, need, dev)
         st = _lib.kdn_layer_norm_backward(n, G, d, code, dy.data_ptr(), x.data_ptr(), wp, mean.data_ptr(), rstd.data_ptr(),

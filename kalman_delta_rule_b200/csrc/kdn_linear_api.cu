@@ -16,6 +16,17 @@ bool aligned(std::initializer_list<const void *> ptrs) {   // 16 bytes; NULL pas
         if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
     return true;
 }
+// no output is an input or another output (kernels read inputs while other CTAs write); NULL passes
+bool distinct(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        for (const void *in : ins)
+            if (*o == in) return false;
+        for (auto other = outs.begin(); other != o; ++other)
+            if (*o == *other) return false;
+    }
+    return true;
+}
 kdn_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? KDN_OK : KDN_ERR_CUDA; }
 
 kdn_status_t check_sizes(int H, int d_k, int d_v, kdn_dtype_t dtype, float scale, int decay) {
@@ -85,9 +96,9 @@ kdn_status_t kdn_linear_forward(const kdn_linear_problem_t *p, const void *q, co
     if (a.nseq == 0 || (a.ntok == 0 && !S_out)) return KDN_OK;
     if (a.ntok > 0 && (!q || !k || !v || !o || (a.decay != KDN_DECAY_NONE && !g))) return KDN_ERR_INVALID_ARG;
     if (!aligned({q, k, v, g, S0, o, S_out})) return KDN_ERR_INVALID_ARG;
-    if (S_out && S_out == S0) return KDN_ERR_INVALID_ARG;
     const size_t need = forward_bytes(p, a);
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return KDN_ERR_WORKSPACE;
+    if (!distinct({a.ntok ? o : nullptr, S_out}, {q, k, v, g, S0})) return KDN_ERR_INVALID_ARG;
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0; a.o = o; a.S_out = S_out;
     a.err = kdn::error_word();
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -104,7 +115,7 @@ kdn_status_t kdn_linear_decode_tokens(int N, int n_tokens, int H, int d_k, int d
     if (N == 0 || n_tokens == 0) return KDN_OK;
     if ((long long)N * n_tokens > (1ll << 30) || (long long)N * H * (d_v / 32) >= (1ll << 31)) return KDN_ERR_UNSUPPORTED;
     if (!q || !k || !v || !S || !o || (decay != KDN_DECAY_NONE && !g)) return KDN_ERR_INVALID_ARG;
-    if (!aligned({q, k, v, g, S, o})) return KDN_ERR_INVALID_ARG;
+    if (!aligned({q, k, v, g, S, o}) || !distinct({o, S}, {q, k, v, g})) return KDN_ERR_INVALID_ARG;
     kdn::LinArgs a{};
     a.q = q; a.k = k; a.v = v; a.g = g; a.decay = decay; a.scale = scale;
     a.S0 = S; a.S_out = S; a.o = o;
@@ -137,10 +148,10 @@ kdn_status_t kdn_linear_backward(const kdn_linear_problem_t *p, const void *q, c
     }
     if (a.ntok > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv || (a.decay != KDN_DECAY_NONE && !g)))
         return KDN_ERR_INVALID_ARG;
-    if (dS0 && dS0 == dS_T) return KDN_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < backward_bytes(p, a) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return KDN_ERR_WORKSPACE;
+    if (a.ntok > 0 ? !distinct({dq, dk, dv, dg, dS0}, {q, k, v, g, S0, d_o, dS_T}) : dS0 == dS_T) return KDN_ERR_INVALID_ARG;
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0;
     a.err = kdn::error_word();
     b.d_o = d_o; b.dS_T = dS_T; b.dq = dq; b.dk = dk; b.dv = dv; b.dg = dg; b.dS0 = dS0;
@@ -154,6 +165,7 @@ kdn_status_t kdn_layer_norm(long long n, int G, int d, kdn_dtype_t dtype, float 
     if (st != KDN_OK) return st;
     if (n == 0) return KDN_OK;
     if (!x || !y || !aligned({x, weight, bias, y, mean, rstd})) return KDN_ERR_INVALID_ARG;
+    if (!distinct({y, mean, rstd}, {x, weight, bias})) return KDN_ERR_INVALID_ARG;
     kdn::NormArgs a{};
     a.x = x; a.weight = weight; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd;
     a.n = n; a.G = G; a.d = d; a.eps = eps;
@@ -188,6 +200,7 @@ kdn_status_t kdn_layer_norm_backward(long long n, int G, int d, kdn_dtype_t dtyp
             return KDN_ERR_WORKSPACE;
         a.part = static_cast<float *>(workspace);
     }
+    if (!distinct({dx, dweight, dbias}, {dy, x, weight, mean, rstd})) return KDN_ERR_INVALID_ARG;
     a.x = x; a.dy = dy; a.weight = weight; a.dx = dx;
     a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
     a.dweight = dweight; a.dbias = dbias;

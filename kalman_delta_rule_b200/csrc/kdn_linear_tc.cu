@@ -75,6 +75,10 @@ struct StateArgs {
     CUtensorMap tx, ty;
 };
 
+// The decay launch before this one is complete.  Every CTA waits for it, one without work too: what the stream runs
+// next must not start with the decay launch still under way because no CTA of this one had anything to do.
+__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // 32 columns of row `row` of a state, in pairs: from the caller's [dk, dv] layout (zero outside it) ...
 __device__ __forceinline__ void load_caller(f32x2 (&S)[16], const float *src, int dk, int dv, int row, int col) {
 #pragma unroll
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     constexpr int W_S = NW_W, W_O = W_S + NW_S, W_MMA = W_O + NW_O, W_TMA = W_MMA + 1;   // MMA beside the rows with the fewest scores
     LinPiece pc;
-    if (!uniform(lin_piece(a, u, f.sp.seg, pc))) return;
+    if (!uniform(lin_piece(a, u, f.sp.seg, pc))) return wait_for_launch();
     const int tok0 = pc.t0 + pc.j * f.sp.seg, len = min(f.sp.seg, pc.len - pc.j * f.sp.seg);
     const int n = uniform((len + C - 1) / C);
 
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
     } else if (warp == W_TMA) {
         // ---------------------------------------------------------- TMA: Q, K and V are refilled as each is free
         if (lane == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");   // the decay records are complete
+            wait_for_launch();                // the decay records are complete
             const Decay *decay = f.decay + (size_t)(lin_first_slot(a, pc.s, pc.t0, C) + pc.j * (f.sp.seg / C)) * a.H + h;
             for (int c = 0; c < n; ++c) {
                 const int st = c & 1, tok = tok0 + c * C;
@@ -495,11 +499,11 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     constexpr int W_MMA = NW_W + NW_S, W_TMA = W_MMA + 1;
     LinPiece pc;
-    if (!uniform(lin_piece(a, u, f.piece, pc))) return;
+    if (!uniform(lin_piece(a, u, f.piece, pc))) return wait_for_launch();
     const int per = f.sp.seg / f.sp.sub;
     if (TOTALS) {
         const int seg = pc.j / per, last = pc.len > 0 ? (pc.len - 1) / f.sp.seg : 0;
-        if (uniform(REV ? seg == 0 : seg == last)) return;
+        if (uniform(REV ? seg == 0 : seg == last)) return wait_for_launch();
     }
     const int tok0 = pc.t0 + pc.j * f.piece, len = min(f.piece, pc.len - pc.j * f.piece);
     const int n = uniform((len + C - 1) / C);
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_cons
         }
     } else if (warp == W_TMA) {
         if (lane == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            wait_for_launch();
             for (int c = 0; c < n; ++c) {
                 const int st = c & 1, tok = tok0 + chunk(c) * C;
                 if (c + 2 < n) {              // (as in the forward)

@@ -102,7 +102,7 @@ def _backward_one(Q, K, V, dO, G, S0, dT, scale, magnitudes=False):
     Z = P * (dO @ V.T)
     ends, starts = (Q * qf).sum(1), (K * kl).sum(1)
     # pairs (query i >= t, key j < t): the strictly-before-t columns of the rows from t on
-    rect = torch.stack([Z[t:, :t].sum() for t in range(L)]) if L else G
+    rect = ((Z.cumsum(1) - Z).flip(0).cumsum(0).flip(0)).diagonal() if L else G
     dg = rect + ends.flip(0).cumsum(0).flip(0) + (starts.cumsum(0) - starts) + (whole * S0 * dT).sum()
     if magnitudes and L:       # what an implementation may sum before it subtracts: the chunk's whole triangle
         dg = dg + torch.stack([Z[t // CHUNK * CHUNK:(t // CHUNK + 1) * CHUNK].sum() for t in range(L)])

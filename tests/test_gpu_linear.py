@@ -347,3 +347,123 @@ def test_refusals(kdn):
         kdn.linear_backward(*a, x["do"].float())
     with pytest.raises(ValueError):
         kdn.linear_decode_tokens(*a, x["S0"][..., :32].contiguous())
+
+
+# Few sequences and heads: bf16 sequences of 2048 tokens and more are cut into segments that are walked at once, from
+# totals of the earlier ones; fp32 ones are scanned.
+LONG = [(1, 2304, 1, 128, 128, None), (2, 4100, 1, 64, 64, None), (1, 3400, 2, 32, 256, [1, 3000, 0, 399]),
+        (1, 2600, 1, 128, 256, [2600]), (1, 2500, 3, 128, 64, [0, 2499, 1]), (1, 2410, 1, 64, 64, [1000, 1010, 400])]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,H,dk,dv,lens", LONG)
+@pytest.mark.parametrize("decay", ["token", "reset", "head", "none"])
+def test_long_sequences(kdn, dtype, B, T, H, dk, dv, lens, decay):
+    cu = offsets(lens) if lens else None
+    x = make(T + dv, B, T, H, dk, dv, dtype, decay, N=len(lens) if lens else B, grads=True)
+    o, S = kdn.linear_forward(x["q"], x["k"], x["v"], x["g"], cu_seqlens=cu, S0=x["S0"], scale=0.5)
+    check_forward(x, o, S, dtype, cu=cu, scale=0.5)
+    out = kdn.linear_backward(x["q"], x["k"], x["v"], x["g"], x["do"], cu_seqlens=cu, S0=x["S0"], dS=x["dS"], scale=0.5)
+    check_backward(x, out, dtype, cu=cu, scale=0.5)
+    kdn.last_device_error()
+
+
+@pytest.mark.parametrize("scale", [-0.7, 0.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_other_scales(kdn, dtype, scale):
+    x = make(67, 1, 200, 2, 64, 64, dtype, grads=True)
+    o, S = kdn.linear_forward(x["q"], x["k"], x["v"], x["g"], S0=x["S0"], scale=scale)
+    check_forward(x, o, S, dtype, scale=scale)
+    out = kdn.linear_backward(x["q"], x["k"], x["v"], x["g"], x["do"], S0=x["S0"], dS=x["dS"], scale=scale)
+    check_backward(x, out, dtype, scale=scale)
+
+
+def test_malformed_offsets_stay_inside_bf16(kdn):
+    """As above on the tensor cores; one long enough to be cut into segments."""
+    for T, bads in ((300, ([0, 500, 90, 330], [-7, 250, 20, 300], [0, 0, 2 ** 30, 300])), (2400, ([0, 2400, 90, 5000], [-7, 2300, 20, 2400]))):
+        x = make(59, 1, T, 1, 64, 128, "bf16", N=3, grads=True)
+        for bad in bads:
+            cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+            kdn.linear_forward(x["q"], x["k"], x["v"], x["g"], cu_seqlens=cu, S0=x["S0"])
+            kdn.linear_backward(x["q"], x["k"], x["v"], x["g"], x["do"], cu_seqlens=cu, S0=x["S0"], dS=x["dS"])
+    torch.cuda.synchronize()
+    kdn.last_device_error()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_offsets_past_32_bits(kdn, dtype):
+    """The last of two packed sequences lies behind 2^31 elements of q; its results are those it has alone."""
+    H, d, n = 64, 32, 300
+    T = (1 << 31) // (H * d) + n + 77
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of device memory")
+    x = make(71, 1, n, H, d, d, dtype, N=1, grads=True)
+    big = {m: torch.zeros((1, T) + x[m].shape[2:], dtype=x[m].dtype, device="cuda") for m in ("q", "k", "v", "g", "do")}
+    for m in big:
+        big[m][:, T - n:] = x[m]
+    cu = offsets([T - n, n])
+    S0, dS = (torch.cat([torch.zeros_like(x[m]), x[m]]) for m in ("S0", "dS"))
+    o, S = kdn.linear_forward(big["q"], big["k"], big["v"], big["g"], cu_seqlens=cu, S0=S0)
+    check_forward(x, o[:, T - n:].contiguous(), S[1:], dtype)
+    assert not o[:, :T - n].any()
+    del o
+    out = kdn.linear_backward(big["q"], big["k"], big["v"], big["g"], big["do"], cu_seqlens=cu, S0=S0, dS=dS)
+    tail = {m: out[m][:, T - n:].contiguous() for m in ("dq", "dk", "dv", "dg")}
+    check_backward(x, {**tail, "dS0": out["dS0"][1:]}, dtype)
+    kdn.last_device_error()
+
+
+def test_decode_states_past_32_bits(kdn):
+    """More than 2^31 elements of state."""
+    N, H, d = 2100, 64, 128
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    x = make(73, 2, 1, H, d, d, "bf16")
+    q, k, v, g, S = (torch.zeros((N,) + t.shape[1:], dtype=t.dtype, device="cuda") for t in (x["q"], x["k"], x["v"], x["g"], x["S0"]))
+    for big, t in ((q, x["q"]), (k, x["k"]), (v, x["v"]), (g, x["g"]), (S, x["S0"])):
+        big[0], big[-1] = t[0], t[1]
+    o = kdn.linear_decode_tokens(q, k, v, g, S)
+    check_forward(x, torch.stack([o[0], o[-1]]), torch.stack([S[0], S[-1]]), "bf16")
+    assert not S[1:-1].any() and not o[1:-1].any()
+
+
+FIRST_USE = """
+import sys, torch
+import kalman_delta_rule_b200.binding as kdn
+dt = getattr(torch, sys.argv[1])
+torch.manual_seed(0)
+r = lambda *s: torch.randn(s, device="cuda").to(dt)
+q, k, v, do = r(1, 2300, 1, 64), r(1, 2300, 1, 64), r(1, 2300, 1, 64), r(1, 2300, 1, 64)
+g = -torch.rand((1, 2300, 1), device="cuda")
+S = torch.zeros((1, 1, 64, 64), device="cuda")
+w = torch.ones(64, device="cuda")
+def calls():
+    o, last = kdn.linear_forward(q, k, v, g)
+    y, mean, rstd = kdn.layer_norm(o, w, w)
+    n = kdn.layer_norm_backward(do, o, w, mean, rstd)
+    b = kdn.linear_backward(q, k, v, g, n["dx"])
+    t = kdn.linear_decode_tokens(q[:, :1].contiguous(), k[:, :1].contiguous(), v[:, :1].contiguous(), g[:, :1].contiguous(), S)
+    return [last, y, n["dweight"], b["dq"], b["dg"], t]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+S.zero_()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+S.zero_()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+kdn.last_device_error()
+print("same")
+"""
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_first_use_inside_a_capture(kdn, dtype):
+    """The process's first call of every operator is captured; its replay gives the eager calls' bits."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_USE, dtype], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

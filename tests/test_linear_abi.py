@@ -124,3 +124,38 @@ def test_norm_arguments(lib):
         assert g(**bad) == B.KDN_ERR_WORKSPACE, bad
     assert g(d=20000) == B.KDN_ERR_UNSUPPORTED
     assert g(n=0, dy=None, x=None, dw=None, ws=None) == B.KDN_OK
+
+
+def test_aliased_outputs(lib):
+    """An output that is an input, or another output, is refused before anything is launched."""
+    at = lambda i: FAKE + (i << 20)                                      # noqa: E731
+    p = problem()
+    need = max(B.kdn_linear_workspace_size(p), B.kdn_linear_backward_workspace_size(p))
+    ws = (at(40), need, None)
+    for i in range(5):             # q, k, v, g, S0
+        for j in (5, 6):           # o, S_out
+            a = [at(n) for n in range(7)]
+            a[j] = a[i]
+            assert B.kdn_linear_forward(p, *a, *ws) == B.KDN_ERR_INVALID_ARG, (i, j)
+    for i in range(12):            # q, k, v, g, S0, d_o, dS_T, then the outputs
+        for j in range(7, 12):
+            if i != j:
+                a = [at(n) for n in range(12)]
+                a[j] = a[i]
+                assert B.kdn_linear_backward(p, *a, *ws) == B.KDN_ERR_INVALID_ARG, (i, j)
+    assert B.kdn_linear_backward(problem(T=0), *[None] * 6, at(1), *[None] * 4, at(1), *ws) == B.KDN_ERR_INVALID_ARG
+    for i in range(4):             # q, k, v, g, S, o
+        for j in (4, 5):
+            a = [at(n) for n in range(6)]
+            a[j] = a[i]
+            assert B.kdn_linear_decode_tokens(2, 1, 2, 64, 64, 1, 1.0, 1, *a, None) == B.KDN_ERR_INVALID_ARG, (i, j)
+    for i in range(3):             # x, weight, bias, y, mean, rstd
+        for j in range(3, 6):
+            a = [at(n) for n in range(6)]
+            a[j] = a[i]
+            assert B.kdn_layer_norm(4, 2, 64, 1, 1e-5, *a, None) == B.KDN_ERR_INVALID_ARG, (i, j)
+    for i in range(5):             # dy, x, weight, mean, rstd, dx, dweight, dbias
+        for j in range(5, 8):
+            a = [at(n) for n in range(8)]
+            a[j] = a[i]
+            assert B.kdn_layer_norm_backward(4, 2, 64, 1, *a, *ws) == B.KDN_ERR_INVALID_ARG, (i, j)
