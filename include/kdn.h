@@ -266,7 +266,7 @@ typedef struct {
     int decay;                      /* kdn_decay_t */
 } kdn_linear_problem_t;
 
-/* Bytes of device workspace of kdn_linear_forward() (host-only). */
+/* Bytes of device workspace of kdn_linear_forward() (host-only; 0 for a few tokens per sequence). */
 kdn_status_t kdn_linear_workspace_size(const kdn_linear_problem_t *p, size_t *bytes);
 
 /* Forward over whole sequences (prompts, training), chunkwise.

@@ -71,11 +71,15 @@ size_t scan_tma_workspace_bytes(long long nchains, long long nchunks_max);
 cudaError_t launch_gain_scan_tma(const ScanArgs &a, long long ntok, void *workspace, cudaStream_t st);
 
 // ---- linear attention with a decay for each head
-// fp32 inputs (and problems without tokens, whatever their type), CUDA cores in chunks of 64 tokens
+// fp32 inputs, CUDA cores in chunks of 64 tokens
 size_t linear_simt_workspace_bytes(const LinArgs &a);
 size_t linear_simt_backward_workspace_bytes(const LinArgs &a);
 cudaError_t launch_linear_simt(const LinArgs &a, void *workspace, cudaStream_t st);
 cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, void *workspace, cudaStream_t st);
+// sequences of at most kLinearShort tokens: one launch, fp32 arithmetic whatever the type
+constexpr int kLinearShort = 16;
+size_t linear_short_backward_workspace_bytes(const LinArgs &a);
+cudaError_t launch_linear_short_backward(const LinBwdArgs &b, bool bf16_in, void *workspace, cudaStream_t st);
 // tensor-core path in chunks of 128 tokens (bf16 inputs)
 size_t linear_tc_workspace_bytes(const LinArgs &a);
 cudaError_t launch_linear_tc(const LinArgs &a, void *workspace, cudaStream_t st);
@@ -83,8 +87,8 @@ size_t linear_tc_backward_workspace_bytes(const LinArgs &a);
 cudaError_t launch_linear_tc_backward(const LinBwdArgs &b, void *workspace, cudaStream_t st);
 // dg [H] of a per-head decay from the shares [slots, H] of chunks of `tokens` tokens, in a fixed order
 cudaError_t launch_linear_head_decay(const LinArgs &a, const float *share, float *dg, int tokens, cudaStream_t st);
-// n tokens of N sequences on a state updated in place
-cudaError_t launch_linear_decode(const LinArgs &a, bool bf16_in, cudaStream_t st);
+// token after token on a state in registers (S_out may be S0)
+cudaError_t launch_linear_recurrent(const LinArgs &a, bool bf16_in, cudaStream_t st);
 
 // ---- layer norm of rows [n, G, d] with a weight and bias row for each of G groups
 struct NormArgs {

@@ -51,20 +51,40 @@ kdn_status_t check_problem(const kdn_linear_problem_t *p, kdn::LinArgs *a) {
     a->scale = p->scale; a->decay = p->decay;
     const long long ntok = (long long)p->B * p->T;
     if (ntok > (1ll << 30)) return KDN_ERR_UNSUPPORTED;
-    // grids are one-dimensional in (slots x heads)
-    if ((ntok / 64 + a->nseq) * a->H >= (1ll << 31)) return KDN_ERR_UNSUPPORTED;
+    // grids are one-dimensional in (slots x heads) or (sequences x heads x tiles of d_v)
+    if ((ntok / 64 + a->nseq) * a->H >= (1ll << 31) || (long long)a->nseq * a->H * (a->dv / 32) >= (1ll << 31)) return KDN_ERR_UNSUPPORTED;
     a->ntok = (int)ntok;
     return KDN_OK;
 }
 
-bool on_tensor_cores(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
-    return p->in_dtype == KDN_DTYPE_BF16 && a.ntok > 0;
+// Which kernels run a problem.  Short sequences, whose lengths are bounded by T (packed: by all the tokens, the lengths
+// being known on the device only), have paths of their own: one launch instead of two to five, no workspace to write and
+// read, and fp32 arithmetic whatever the type -- with a handful of tokens nothing would average the tensor cores' roundings.
+// Forward, token after token.  At d = 128 with 1 / 64 / 2048 heads in all: bf16 16 tokens 5.2 / 7.2 / 104 us against 8.9 /
+// 9.4 / 229 on the tensor cores, 24 tokens 6.9 / 9.6 / 145, 64 tokens 15.5 / 21 / 329 against 8.7 / 9.4 / 230; fp32 64
+// tokens 15.2 / 21 / 310 against 32 / 38 / 1172 in chunks, 128 tokens 31 / 44 / 642 against 32 / 63 / 2187.
+// Backward, the whole sequence as one chunk: 1 token 13.8 / 14.0 / 144 us, 16 tokens 27 / 28 / 291 against 26 / 28 / 547 on
+// the tensor cores (fp32: 62 / 77 / 1506 in chunks); its shared memory holds 16.
+constexpr int kShortForwardBf16 = 24, kShortForwardF32 = 64;
+enum Path { SHORT, CUDA_CORES, TENSOR_CORES };
+int longest(const kdn::LinArgs &a) { return a.cu ? a.ntok : a.T; }
+Path forward_path(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
+    const bool bf16 = p->in_dtype == KDN_DTYPE_BF16;
+    if (longest(a) <= (bf16 ? kShortForwardBf16 : kShortForwardF32)) return SHORT;
+    return bf16 ? TENSOR_CORES : CUDA_CORES;
+}
+Path backward_path(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
+    if (longest(a) <= kdn::kLinearShort) return SHORT;
+    return p->in_dtype == KDN_DTYPE_BF16 ? TENSOR_CORES : CUDA_CORES;
 }
 size_t forward_bytes(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
-    return on_tensor_cores(p, a) ? kdn::linear_tc_workspace_bytes(a) : kdn::linear_simt_workspace_bytes(a);
+    const Path path = forward_path(p, a);
+    return path == SHORT ? 0 : path == TENSOR_CORES ? kdn::linear_tc_workspace_bytes(a) : kdn::linear_simt_workspace_bytes(a);
 }
 size_t backward_bytes(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {
-    return on_tensor_cores(p, a) ? kdn::linear_tc_backward_workspace_bytes(a) : kdn::linear_simt_backward_workspace_bytes(a);
+    const Path path = backward_path(p, a);
+    return path == SHORT ? kdn::linear_short_backward_workspace_bytes(a)
+                         : path == TENSOR_CORES ? kdn::linear_tc_backward_workspace_bytes(a) : kdn::linear_simt_backward_workspace_bytes(a);
 }
 
 kdn_status_t check_norm(long long n, int G, int d, kdn_dtype_t dtype, float eps) {
@@ -102,8 +122,11 @@ kdn_status_t kdn_linear_forward(const kdn_linear_problem_t *p, const void *q, co
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0; a.o = o; a.S_out = S_out;
     a.err = kdn::error_word();
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (on_tensor_cores(p, a)) return cuda_status(kdn::launch_linear_tc(a, workspace, cs));
-    return cuda_status(kdn::launch_linear_simt(a, workspace, cs));
+    switch (forward_path(p, a)) {
+        case SHORT: return cuda_status(kdn::launch_linear_recurrent(a, p->in_dtype == KDN_DTYPE_BF16, cs));
+        case CUDA_CORES: return cuda_status(kdn::launch_linear_simt(a, workspace, cs));
+        default: return cuda_status(kdn::launch_linear_tc(a, workspace, cs));
+    }
 }
 
 kdn_status_t kdn_linear_decode_tokens(int N, int n_tokens, int H, int d_k, int d_v, kdn_dtype_t in_dtype, float scale,
@@ -120,7 +143,7 @@ kdn_status_t kdn_linear_decode_tokens(int N, int n_tokens, int H, int d_k, int d
     a.q = q; a.k = k; a.v = v; a.g = g; a.decay = decay; a.scale = scale;
     a.S0 = S; a.S_out = S; a.o = o;
     a.T = n_tokens; a.nseq = N; a.H = H; a.dk = d_k; a.dv = d_v; a.ntok = N * n_tokens;
-    return cuda_status(kdn::launch_linear_decode(a, in_dtype == KDN_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
+    return cuda_status(kdn::launch_linear_recurrent(a, in_dtype == KDN_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 kdn_status_t kdn_linear_backward_workspace_size(const kdn_linear_problem_t *p, size_t *bytes) {
@@ -155,8 +178,11 @@ kdn_status_t kdn_linear_backward(const kdn_linear_problem_t *p, const void *q, c
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0;
     a.err = kdn::error_word();
     b.d_o = d_o; b.dS_T = dS_T; b.dq = dq; b.dk = dk; b.dv = dv; b.dg = dg; b.dS0 = dS0;
-    if (on_tensor_cores(p, a)) return cuda_status(kdn::launch_linear_tc_backward(b, workspace, cs));
-    return cuda_status(kdn::launch_linear_simt_backward(b, workspace, cs));
+    switch (backward_path(p, a)) {
+        case SHORT: return cuda_status(kdn::launch_linear_short_backward(b, p->in_dtype == KDN_DTYPE_BF16, workspace, cs));
+        case CUDA_CORES: return cuda_status(kdn::launch_linear_simt_backward(b, workspace, cs));
+        default: return cuda_status(kdn::launch_linear_tc_backward(b, workspace, cs));
+    }
 }
 
 kdn_status_t kdn_layer_norm(long long n, int G, int d, kdn_dtype_t dtype, float eps, const void *x, const float *weight,

@@ -34,7 +34,7 @@ def offsets(lens):
     return torch.tensor([0] + list(itertools.accumulate(lens)), dtype=torch.int32).cuda()
 
 
-def check_forward(x, o, S, dtype, cu=None, scale=1.0, mask=None):
+def check_forward(x, o, S, dtype, cu=None, scale=1.0, mask=None, state=True):
     r = R.forward(x["q"], x["k"], x["v"], x["g"], cu=cu, S0=x["S0"], scale=scale)
     T, dk, dv = x["q"].shape[1], x["q"].shape[-1], x["v"].shape[-1]
     n = R.terms(T, dk, dv) * R.U32
@@ -43,7 +43,8 @@ def check_forward(x, o, S, dtype, cu=None, scale=1.0, mask=None):
         bound = bound * (1 + R.U16) + R.U16 * (r["o"].abs() + (1 + R.U16) * r["round_o"])
     rows = slice(None) if mask is None else mask
     R.assert_within(o.float().cpu()[:, rows], r["o"][:, rows], bound[:, rows], "o")
-    R.assert_within(S, r["S"], n * r["mag_S"], "S")
+    if state:
+        R.assert_within(S, r["S"], n * r["mag_S"], "S")
 
 
 def check_backward(x, out, dtype, cu=None, scale=1.0):
@@ -340,7 +341,8 @@ def test_refusals(kdn):
     with pytest.raises(kdn.KdnError):
         kdn.linear_forward(*a, S0=x["S0"], S_out=x["S0"])
     with pytest.raises(kdn.KdnError):
-        kdn.linear_forward(*a, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        y = make(61, 2, 200, 2, 64, 64, "bf16")     # (a few tokens need no workspace)
+        kdn.linear_forward(y["q"], y["k"], y["v"], y["g"], workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         kdn.linear_backward(*a, x["do"][:, :4].contiguous())
     with pytest.raises(TypeError):
@@ -366,6 +368,53 @@ def test_long_sequences(kdn, dtype, B, T, H, dk, dv, lens, decay):
     out = kdn.linear_backward(x["q"], x["k"], x["v"], x["g"], x["do"], cu_seqlens=cu, S0=x["S0"], dS=x["dS"], scale=0.5)
     check_backward(x, out, dtype, cu=cu, scale=0.5)
     kdn.last_device_error()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", SIZES)
+@pytest.mark.parametrize("B,T,lens", [(3, 1, None), (5, 16, None), (2, 17, None), (2, 24, None), (1, 16, [0, 5, 0, 10, 1, 0]),
+                                      (1, 16, [3, 4, 2]), (1, 24, [7, 0, 16]), (2, 64, None), (2, 65, None)])
+@pytest.mark.parametrize("decay", ["token", "reset", "head", "none"])
+def test_short_sequences(kdn, dtype, dk, dv, B, T, lens, decay):
+    """Around the lengths at which the path changes; packed ones with empty sequences and rows behind the last."""
+    cu = offsets(lens) if lens else None
+    end = sum(lens) if lens else T
+    x = make(T + dk, B, T, 3, dk, dv, dtype, decay, N=len(lens) if lens else B, grads=True)
+    if end < T:
+        for m in ("q", "k", "v", "do"):
+            x[m][:, end:] = float("nan")
+    o = torch.full_like(x["v"], 7.0)
+    _, S = kdn.linear_forward(x["q"], x["k"], x["v"], x["g"], cu_seqlens=cu, S0=x["S0"], scale=0.8, o=o)
+    check_forward(x, o, S, dtype, cu=cu, scale=0.8, mask=slice(0, end))
+    assert (o[:, end:] == 7.0).all()
+    out = kdn.linear_backward(x["q"], x["k"], x["v"], x["g"], x["do"], cu_seqlens=cu, S0=x["S0"], dS=x["dS"], scale=0.8)
+    cut = {m: t[:, :end].contiguous() if m in ("q", "k", "v", "do") or m == "g" and t is not None and t.dim() == 3 else t for m, t in x.items()}
+    out = {m: t[:, :end].contiguous() if m in ("dq", "dk", "dv") or m == "dg" and t.dim() == 3 else t for m, t in out.items()}
+    check_backward(cut, out, dtype, cu=cu, scale=0.8)
+    plain, none = kdn.linear_forward(x["q"], x["k"], x["v"], x["g"], cu_seqlens=cu, want_state=False)
+    assert none is None
+    check_forward({**x, "S0": None}, plain, torch.zeros(0), dtype, cu=cu, mask=slice(0, end), state=False)
+    out = kdn.linear_backward(x["q"], x["k"], x["v"], x["g"], x["do"], cu_seqlens=cu, want_initial=False)
+    assert "dS0" not in out
+    kdn.last_device_error()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [5, 16, 40])
+def test_bad_values_in_short_sequences(kdn, dtype, T):
+    """A NaN log decay, and infinities and NaN in one sequence: the others' results keep their bits."""
+    x = make(79 + T, 3, T, 2, 64, 64, dtype, grads=True)
+    run = lambda: (kdn.linear_forward(x["q"], x["k"], x["v"], x["g"], S0=x["S0"]),                        # noqa: E731
+                   kdn.linear_backward(x["q"], x["k"], x["v"], x["g"], x["do"], S0=x["S0"], dS=x["dS"]))
+    (o, S), g = run()
+    x["g"][1, T // 2] = float("nan")
+    x["v"][1, 0] = float("inf")
+    x["do"][1, T - 1] = float("nan")
+    (o2, S2), g2 = run()
+    for i in (0, 2):
+        assert torch.equal(o[i], o2[i]) and torch.equal(S[i], S2[i])
+        assert all(torch.equal(g[n][i], g2[n][i]) for n in g)
+    assert o2[1, T // 2:].isnan().all() and S2[1].isnan().all()
 
 
 @pytest.mark.parametrize("scale", [-0.7, 0.0])
