@@ -77,7 +77,7 @@ size_t linear_simt_backward_workspace_bytes(const LinArgs &a);
 cudaError_t launch_linear_simt(const LinArgs &a, void *workspace, cudaStream_t st);
 cudaError_t launch_linear_simt_backward(const LinBwdArgs &b, void *workspace, cudaStream_t st);
 // sequences of at most kLinearShort tokens: one launch, fp32 arithmetic whatever the type
-constexpr int kLinearShort = 16;
+constexpr int kLinearShort = 32;
 size_t linear_short_backward_workspace_bytes(const LinArgs &a);
 cudaError_t launch_linear_short_backward(const LinBwdArgs &b, bool bf16_in, void *workspace, cudaStream_t st);
 // tensor-core path in chunks of 128 tokens (bf16 inputs)

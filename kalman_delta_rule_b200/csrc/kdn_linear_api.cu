@@ -58,14 +58,15 @@ kdn_status_t check_problem(const kdn_linear_problem_t *p, kdn::LinArgs *a) {
 }
 
 // Which kernels run a problem.  Short sequences, whose lengths are bounded by T (packed: by all the tokens, the lengths
-// being known on the device only), have paths of their own: one launch instead of two to five, no workspace to write and
-// read, and fp32 arithmetic whatever the type -- with a handful of tokens nothing would average the tensor cores' roundings.
-// Forward, token after token.  At d = 128 with 1 / 64 / 2048 heads in all: bf16 16 tokens 5.2 / 7.2 / 104 us against 8.9 /
-// 9.4 / 229 on the tensor cores, 24 tokens 6.9 / 9.6 / 145, 64 tokens 15.5 / 21 / 329 against 8.7 / 9.4 / 230; fp32 64
-// tokens 15.2 / 21 / 310 against 32 / 38 / 1172 in chunks, 128 tokens 31 / 44 / 642 against 32 / 63 / 2187.
-// Backward, the whole sequence as one chunk: 1 token 13.8 / 14.0 / 144 us, 16 tokens 27 / 28 / 291 against 26 / 28 / 547 on
-// the tensor cores (fp32: 62 / 77 / 1506 in chunks); its shared memory holds 16.
-constexpr int kShortForwardBf16 = 24, kShortForwardF32 = 64;
+// being known on the device only), have paths of their own: one launch instead of two to five, no states written and read
+// between launches, and fp32 arithmetic whatever the type -- with a few hundred scores nothing averages the tensor cores'
+// roundings of them.  At d = 128, with 1 / 64 / 2048 heads in all:
+// Forward, token after token: 16 tokens 5.2 / 7.0 / 99 us in bf16 against 9.2 / 9.5 / 229 on the tensor cores, 32 tokens
+// 8.6 / 11.6 / 177 against 9.1 / 9.5 / 228, 64 tokens 15.5 / 21 / 329 against 8.7 / 9.4 / 230.  fp32, 64 tokens: 15.2 / 21 / 310
+// against 32 / 38 / 1172 in chunks; one head of d = 64 meets them at 128 tokens (25 against 22).
+// Backward, the whole sequence as one chunk: 16 tokens 24 / 24 / 271 us against 27 / 28 / 544 on the tensor cores, 32 tokens
+// 39 / 40 / 584 against 27 / 28 / 541 (d = 64: 17 / 17 / 255 against 23 / 23 / 302; fp32 in chunks: 65 / 79 / 1563).
+constexpr int kShortForwardBf16 = 32, kShortForwardF32 = 64;
 enum Path { SHORT, CUDA_CORES, TENSOR_CORES };
 int longest(const kdn::LinArgs &a) { return a.cu ? a.ntok : a.T; }
 Path forward_path(const kdn_linear_problem_t *p, const kdn::LinArgs &a) {

@@ -21,7 +21,7 @@ constexpr int NT = 256;
 }
 
 template <int DK, int DVT, int GT, typename Tin>
-__global__ void __launch_bounds__(NT, 2) linear_recurrent_kernel(LinArgs a)
+__global__ void __launch_bounds__(NT, GT == 1 ? 1 : 2) linear_recurrent_kernel(LinArgs a)
 {
     constexpr int TPR = DVT / 4;           // threads per row of S
     constexpr int RPP = NT / TPR;          // rows per pass
@@ -41,13 +41,11 @@ __global__ void __launch_bounds__(NT, 2) linear_recurrent_kernel(LinArgs a)
     lin_seq(a, s, t0, len);
 
     const size_t base = (size_t)sh * DK * a.dv + col + c4;
-    f32x2 S[NP][2];
+    float4 S[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const int row = p * RPP + rs;
-        const float4 x = a.S0 ? __ldcs(reinterpret_cast<const float4 *>(a.S0 + base + (size_t)row * a.dv)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        S[p][0] = pk2(x.x, x.y);
-        S[p][1] = pk2(x.z, x.w);
+        S[p] = a.S0 ? __ldcs(reinterpret_cast<const float4 *>(a.S0 + base + (size_t)row * a.dv)) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     // the next group of tokens, on its way while this one is at work (behind the end: whatever was there before)
     float q1[NQ] = {}, k1[NQ] = {}, v1[NV] = {}, g1 = 0.f;
@@ -87,18 +85,30 @@ __global__ void __launch_bounds__(NT, 2) linear_recurrent_kernel(LinArgs a)
         for (int j = 0; j < GT; ++j) {
             if (i0 + j >= len) break;
             const float4 v = *reinterpret_cast<const float4 *>(&vs[j][c4]);
-            const f32x2 f2 = pk2(fs[j], fs[j]), v01 = pk2(v.x, v.y), v23 = pk2(v.z, v.w);
-            f32x2 o01 = 0, o23 = 0;
+            const float f = fs[j];
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if constexpr (GT == 1) {       // HBM's time, not arithmetic's: one element at a time takes fewer registers
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const float2 c = qk[j][p * RPP + rs];
-                const f32x2 q2 = pk2(c.x, c.x), k2 = pk2(c.y, c.y);
-                S[p][0] = fma2(k2, v01, mul2(f2, S[p][0]));
-                S[p][1] = fma2(k2, v23, mul2(f2, S[p][1]));
-                o01 = fma2(q2, S[p][0], o01);
-                o23 = fma2(q2, S[p][1], o23);
+                for (int p = 0; p < NP; ++p) {
+                    const float2 c = qk[j][p * RPP + rs];
+                    float4 &x = S[p];
+                    x = make_float4(fmaf(c.y, v.x, f * x.x), fmaf(c.y, v.y, f * x.y), fmaf(c.y, v.z, f * x.z), fmaf(c.y, v.w, f * x.w));
+                    o = make_float4(fmaf(c.x, x.x, o.x), fmaf(c.x, x.y, o.y), fmaf(c.x, x.z, o.z), fmaf(c.x, x.w, o.w));
+                }
+            } else {
+                const f32x2 f2 = pk2(f, f), v01 = pk2(v.x, v.y), v23 = pk2(v.z, v.w);
+                f32x2 o01 = 0, o23 = 0;
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    const float2 c = qk[j][p * RPP + rs];
+                    const f32x2 q2 = pk2(c.x, c.x), k2 = pk2(c.y, c.y);
+                    const f32x2 x01 = fma2(k2, v01, mul2(f2, pk2(S[p].x, S[p].y))), x23 = fma2(k2, v23, mul2(f2, pk2(S[p].z, S[p].w)));
+                    o01 = fma2(q2, x01, o01);
+                    o23 = fma2(q2, x23, o23);
+                    S[p] = make_float4(x2(x01), y2(x01), x2(x23), y2(x23));
+                }
+                o = make_float4(x2(o01), y2(o01), x2(o23), y2(o23));
             }
-            float4 o = make_float4(x2(o01), y2(o01), x2(o23), y2(o23));
 #pragma unroll
             for (int off = TPR; off < 32; off <<= 1) {    // rows of the same warp
                 o.x += __shfl_xor_sync(0xffffffffu, o.x, off);
@@ -122,8 +132,7 @@ __global__ void __launch_bounds__(NT, 2) linear_recurrent_kernel(LinArgs a)
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const int row = p * RPP + rs;
-        __stcs(reinterpret_cast<float4 *>(a.S_out + base + (size_t)row * a.dv),
-               make_float4(x2(S[p][0]), y2(S[p][0]), x2(S[p][1]), y2(S[p][1])));
+        __stcs(reinterpret_cast<float4 *>(a.S_out + base + (size_t)row * a.dv), S[p]);
     }
 }
 

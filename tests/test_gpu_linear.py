@@ -372,7 +372,7 @@ def test_long_sequences(kdn, dtype, B, T, H, dk, dv, lens, decay):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("dk,dv", SIZES)
-@pytest.mark.parametrize("B,T,lens", [(3, 1, None), (5, 16, None), (2, 17, None), (2, 24, None), (1, 16, [0, 5, 0, 10, 1, 0]),
+@pytest.mark.parametrize("B,T,lens", [(3, 1, None), (5, 16, None), (2, 17, None), (2, 24, None), (2, 32, None), (2, 33, None), (1, 32, [0, 30, 0, 2]), (1, 16, [0, 5, 0, 10, 1, 0]),
                                       (1, 16, [3, 4, 2]), (1, 24, [7, 0, 16]), (2, 64, None), (2, 65, None)])
 @pytest.mark.parametrize("decay", ["token", "reset", "head", "none"])
 def test_short_sequences(kdn, dtype, dk, dv, B, T, lens, decay):
