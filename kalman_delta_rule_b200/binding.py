@@ -374,8 +374,11 @@ def gain_scan(k, alpha, sigma, r, cu_seqlens=None, P0=None, mu: float = 1.0, chu
 
 
 # ------------------------------------------------------------------ linear attention, layer norm
-# These wrappers serve single-token decoding too, where the launch takes a few microseconds: what they do per call
-# is kept short (one pass of checks, no context managers unless another device or stream is asked for).
+# These wrappers serve single-token decoding too, where the kernel takes a few microseconds.  The common call --
+# contiguous tensors of the expected types and shapes on the current device, its current stream, no caller's workspace --
+# goes from the tensors to the C ABI in one native step (csrc/kdn_marshal.cpp).  For any other that returns None, and
+# the code here checks, dispatches and raises.
+_native_mod = None
 _mod = None
 _raw_stream = None   # device index -> handle of its current stream
 
@@ -390,6 +393,26 @@ def _cuda():
             (lambda index: torch.cuda.current_stream(index).cuda_stream)
         _mod = torch
     return _mod
+
+
+def _native():
+    """The extension module, bound to the loaded library's functions."""
+    global _native_mod
+    if _native_mod is None:
+        lib = load()
+        _cuda()
+        path = os.path.join(PKG, "_kdn_marshal.so")
+        if not os.path.exists(path):
+            raise FileNotFoundError(f"{path} not built; run `python -m kalman_delta_rule_b200.build`")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("_kdn_marshal", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        names = ("linear_workspace_size", "linear_forward", "linear_decode_tokens", "linear_backward_workspace_size",
+                 "linear_backward", "layer_norm", "layer_norm_backward_workspace_size", "layer_norm_backward")
+        mod.bind(*(ctypes.cast(getattr(lib, "kdn_" + n), _vp).value for n in names))
+        _native_mod = mod
+    return _native_mod
 
 
 def _type_of(torch, name, t):
@@ -503,6 +526,10 @@ def linear_forward(q, k, v, g=None, cu_seqlens=None, S0=None, scale: float = 1.0
     q, k [B,T,H,dk] and v [B,T,H,dv] in bf16 or fp32; g the fp32 log decay, [B,T,H], [H] or None (no
     decay); varlen: B = 1 with int32 cu_seqlens; S0 [N,H,dk,dv] fp32.  Returns (o, S_out); outputs
     and workspace are allocated when not given (S_out stays None without ``want_state``)."""
+    if stream is None and workspace is None:
+        done = (_native_mod or _native()).linear_forward(q, k, v, g, cu_seqlens, S0, scale, o, S_out, want_state)
+        if done is not None:
+            return done
     torch, dev, p, states, gp = _linear_problem(q, k, v, g, cu_seqlens, scale)
     s0 = _state_ptr(torch, "S0", S0, states, dev)
     if o is not None:
@@ -529,6 +556,10 @@ def linear_forward(q, k, v, g=None, cu_seqlens=None, S0=None, scale: float = 1.0
 def linear_decode_tokens(q, k, v, g, S, scale: float = 1.0, o=None, stream=None):
     """n tokens per sequence of the recurrent form in one launch on [N, n, H, d] token tensors
     (kdn_linear_decode_tokens); g [N, n, H], [H] or None; S [N,H,dk,dv] fp32, updated in place."""
+    if stream is None:
+        done = (_native_mod or _native()).linear_decode(q, k, v, g, S, scale, o, 4)
+        if done is not None:
+            return done
     torch, dev, p, states, gp = _linear_problem(q, k, v, g, None, scale)
     _expect("S", S, states, torch.float32, dev)
     if o is not None:
@@ -549,6 +580,10 @@ def linear_decode_tokens(q, k, v, g, S, scale: float = 1.0, o=None, stream=None)
 def linear_decode_step(q, k, v, g, S, scale: float = 1.0, o=None, stream=None):
     """One token of the recurrent form on [N, H, d] token tensors; g [N, H], [H] or None.  A one-dimensional
     g is the per-head decay."""
+    if stream is None:
+        done = (_native_mod or _native()).linear_decode(q, k, v, g, S, scale, o, 3)
+        if done is not None:
+            return done
     g4 = g if g is None or g.dim() == 1 else g.unsqueeze(1)
     o4 = None if o is None else o.unsqueeze(1)
     return linear_decode_tokens(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g4, S, scale=scale, o=o4,
@@ -561,6 +596,10 @@ def linear_backward(q, k, v, g, d_o, cu_seqlens=None, S0=None, dS=None, scale: f
 
     Returns a dict: dq, dk, dv (shapes and type of q, k, v), with a decay dg (fp32, shape of g), and with
     ``want_initial`` dS0 [N,H,dk,dv] fp32.  The workspace is allocated when not given."""
+    if stream is None and workspace is None:
+        done = (_native_mod or _native()).linear_backward(q, k, v, g, d_o, cu_seqlens, S0, dS, scale, want_initial)
+        if done is not None:
+            return done
     torch, dev, p, states, gp = _linear_problem(q, k, v, g, cu_seqlens, scale)
     _expect("d_o", d_o, v.shape, q.dtype, dev)
     s0, ds = _state_ptr(torch, "S0", S0, states, dev), _state_ptr(torch, "dS", dS, states, dev)
@@ -605,6 +644,10 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, y=None, stream=None
     x.shape[:-1].  weight, bias: fp32 [d], or [G, d] for x [..., G, d] (a row for each head), or None.
     (``layer_norm_backward`` returns the bias's gradient beside the weight's: a norm that trains a bias alone has
     a weight of ones.)"""
+    if stream is None:
+        done = (_native_mod or _native()).layer_norm(x, weight, bias, eps, y)
+        if done is not None:
+            return done
     torch = _mod or _cuda()
     code = _type_of(torch, "x", x)
     dev = _device_of("x", x)
@@ -639,6 +682,10 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, y=None, stream=None
 def layer_norm_backward(dy, x, weight, mean, rstd, workspace=None, stream=None):
     """Gradients of <y, dy> for ``layer_norm`` (kdn_layer_norm_backward), mean and rstd as it returned
     them: a dict of dx and, with a weight, dweight and dbias (fp32, the weight's shape)."""
+    if stream is None and workspace is None:
+        done = (_native_mod or _native()).layer_norm_backward(dy, x, weight, mean, rstd)
+        if done is not None:
+            return done
     torch = _mod or _cuda()
     code = _type_of(torch, "x", x)
     dev = _device_of("x", x)

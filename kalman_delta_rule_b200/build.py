@@ -2,6 +2,8 @@
 
 Each ``csrc/*.cu`` is compiled to an object in ``_build/`` (in parallel, only when it
 or a header changed) and the objects are linked into ``kalman_delta_rule_b200/libkdn.so``.
+``csrc/kdn_marshal.cpp`` (the binding's native path from torch tensors to the C ABI; host code only)
+becomes the extension module ``_kdn_marshal.so`` beside it, with g++ and torch's headers.
 Usage: ``python -m kalman_delta_rule_b200.build [--force] [--verbose]``.
 """
 from __future__ import annotations
@@ -16,6 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libkdn.so")
+MARSHAL = os.path.join(PKG, "_kdn_marshal.so")
 OBJ_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -31,6 +34,31 @@ def _nvcc() -> str:
 def _headers():
     return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
+
+
+def build_marshal(force: bool = False) -> str:
+    """The binding's extension module (torch's headers and libraries, the running interpreter's ABI)."""
+    src = os.path.join(CSRC, "kdn_marshal.cpp")
+    newest = max(os.path.getmtime(p) for p in (src, __file__, os.path.join(ROOT, "include", "kdn.h")))
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    inc = [os.path.join(ROOT, "include"), os.path.join(home, "include"),
+           os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += ["-I" + i for i in inc] + [src, "-o", tmp, "-L" + os.path.join(home, "lib"), "-Wl,-rpath," + os.path.join(home, "lib")]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{p.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -49,8 +77,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{p.stderr}")
         return obj, p.stderr
 
-    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        marshal = ex.submit(build_marshal, force)
         results = list(ex.map(compile_one, srcs))
+        marshal.result()
     objs = [o for o, _ in results]
     if verbose:
         for o, log in results:

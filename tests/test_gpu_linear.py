@@ -476,6 +476,40 @@ def test_decode_states_past_32_bits(kdn):
     assert not S[1:-1].any() and not o[1:-1].any()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_both_ways_to_the_abi(kdn, dtype):
+    """The wrappers' native step takes the common call and leaves any other to Python (here: a stream, a workspace of
+    the caller's, an integer factor): the same bits, the same shapes, and the caller's outputs are the ones written."""
+    x = make(83, 2, 70, 2, 64, 32, dtype, grads=True)
+    a, st = (x["q"], x["k"], x["v"], x["g"]), torch.cuda.current_stream()
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    o, S = kdn.linear_forward(*a, S0=x["S0"])
+    mine = torch.empty_like(o), torch.empty_like(S)
+    for kw in (dict(stream=st), dict(workspace=ws), dict(scale=1), dict(o=mine[0], S_out=mine[1])):
+        o2, S2 = kdn.linear_forward(*a, S0=x["S0"], **kw)
+        assert torch.equal(o, o2) and torch.equal(S, S2)
+    assert o2 is mine[0] and S2 is mine[1]
+    assert kdn.linear_forward(*a, want_state=False)[1] is None and kdn.linear_forward(*a, want_state=0, stream=st)[1] is None
+    g = kdn.linear_backward(*a, x["do"], S0=x["S0"], dS=x["dS"])
+    for kw in (dict(stream=st), dict(workspace=ws), dict(scale=1)):
+        g2 = kdn.linear_backward(*a, x["do"], S0=x["S0"], dS=x["dS"], **kw)
+        assert g.keys() == g2.keys() and all(torch.equal(g[n], g2[n]) and g[n].dtype == g2[n].dtype for n in g)
+    assert "dg" not in kdn.linear_backward(*a[:3], None, x["do"], want_initial=False)
+    T1 = [t[:, 0].contiguous() for t in a]
+    S1, S2, S3 = x["S0"].clone(), x["S0"].clone(), x["S0"].clone()
+    o1, o2 = kdn.linear_decode_step(*T1, S1), kdn.linear_decode_step(*T1, S2, stream=st)
+    o3 = kdn.linear_decode_tokens(*(t.unsqueeze(1) for t in T1), S3)
+    assert o1.shape == (2, 2, 32) and torch.equal(o1, o2) and torch.equal(o1, o3.squeeze(1)) and torch.equal(S1, S2) and torch.equal(S1, S3)
+    w = torch.randn((2, 32), device="cuda")
+    for args in ((x["v"], w, w), (x["v"], None, w), (x["v"], w[0].contiguous(), None), (x["v"][0, 0, 0].contiguous(), None, None)):
+        y, m, r = kdn.layer_norm(*args)
+        y2, m2, r2 = kdn.layer_norm(*args, stream=st)
+        assert torch.equal(y, y2) and torch.equal(m, m2) and torch.equal(r, r2) and m.shape == m2.shape == args[0].shape[:-1]
+        d, d2 = (kdn.layer_norm_backward(y, args[0], args[1], m, r, **kw) for kw in ({}, dict(stream=st)))
+        assert d.keys() == d2.keys() and all(torch.equal(d[n], d2[n]) for n in d)
+    kdn.last_device_error()
+
+
 FIRST_USE = """
 import sys, torch
 import kalman_delta_rule_b200.binding as kdn
