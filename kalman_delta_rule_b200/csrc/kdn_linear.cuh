@@ -117,4 +117,25 @@ __device__ __forceinline__ float2 lin_chunk_decay(Log2 x) {
 }
 __device__ __forceinline__ float lin_carry(float2 decay, float s, float u) { return fmaf(decay.x, s, fmaf(decay.y, s, u)); }
 
+// Launches of a call follow one another programmatically: a CTA of the next one may start, set itself up and read the
+// caller's inputs once every CTA of this one runs (or is done).  Every CTA waits for the launch before it, one without
+// work too, before it reads what any earlier launch wrote: no launch is complete before those that precede it.
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace kdn

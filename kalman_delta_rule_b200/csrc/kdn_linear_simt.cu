@@ -137,6 +137,7 @@ struct Walks {
 template <int DK, int DVT>
 __global__ void __launch_bounds__(NT) linear_delta_kernel(LinArgs a, Walks ws, float2 *dec)
 {
+    let_next_launch();
     extern __shared__ __align__(16) float sm[];
     float *Xs = sm, *Ys = sm + C * (DK + PAD);
     __shared__ ChunkDecay dec_s;
@@ -179,6 +180,8 @@ __global__ void __launch_bounds__(NT) linear_delta_kernel(LinArgs a, Walks ws, f
 // eight at a time, so that the loads of a group overlap and only its multiply-adds are serial
 __global__ void __launch_bounds__(256) linear_scan_kernel(LinArgs a, Walks ws, const float2 *dec)
 {
+    let_next_launch();
+    wait_for_launch();
     const bool rev = blockIdx.z != 0;
     const Walk &wk = ws.w[blockIdx.z];
     const int per = a.dk * a.dv / 4;
@@ -230,11 +233,12 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
     const Log2 *G = dec_s.G;
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H, col = blockIdx.y * DVT;
     LinPiece p;
-    if (!lin_piece(a, u, C, p) || p.len == 0) return;
+    if (!lin_piece(a, u, C, p) || p.len == 0) return wait_for_launch();
     const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
     load_rows<DK>(Qs, a.q, tok, L, a.H, h, DK, 0);
     load_rows<DK>(Ks, a.k, tok, L, a.H, h, DK, 0);
     load_rows<DVT>(Vs, a.v, tok, L, a.H, h, a.dv, col);
+    wait_for_launch();                     // the states are complete
     load_state<DK, DVT>(Ss, S + ((size_t)u * a.H + h) * DK * a.dv + col, a.dv);
     chunk_log_decay(a, tok, L, h, &dec_s);
     const float scale = a.scale * dec_s.one;
@@ -291,7 +295,7 @@ __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBw
     __shared__ float zr[C], zc[8][C], xi[C], yi[C], wsum[8];
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H;
     LinPiece p;
-    if (!lin_piece(a, u, C, p) || p.len == 0) return;
+    if (!lin_piece(a, u, C, p) || p.len == 0) return wait_for_launch();
     const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const size_t sbase = ((size_t)u * a.H + h) * DK * a.dv;
@@ -313,6 +317,7 @@ __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBw
 
     float dp[4][4] = {}, dqi[4][NK] = {}, dki[4][NK] = {};
     float sr = 0.f;
+    wait_for_launch();                     // the states and their gradients are complete
     for (int col = 0; col < a.dv; col += DVT) {
         __syncthreads();       // the previous tile is read; Ps is written
         load_rows<DVT>(Vs, a.v, tok, L, a.H, h, a.dv, col);
@@ -480,8 +485,7 @@ cudaError_t states(const LinArgs &a, const Walks &ws, int walks, float2 *dec, cu
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long threads = (long long)a.nseq * a.H * (a.dk * a.dv / 4);
-    linear_scan_kernel<<<dim3((unsigned)((threads + 255) / 256), 1, walks), 256, 0, st>>>(a, ws, dec);
-    return cudaGetLastError();
+    return launch_next(linear_scan_kernel, dim3((unsigned)((threads + 255) / 256), 1, walks), 256, 0, st, a, ws, (const float2 *)dec);
 }
 
 template <int DK, int DVT>
@@ -495,8 +499,7 @@ cudaError_t forward(const LinArgs &a, uint8_t *ws, cudaStream_t st) {
     auto kern = linear_out_kernel<DK, DVT>;
     e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT), NT, smem, st>>>(a, U);
-    return cudaGetLastError();
+    return launch_next(kern, dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT), NT, smem, st, a, (const float *)U);
 }
 
 template <int DK, int DVT>
@@ -515,8 +518,7 @@ cudaError_t backward(const LinBwdArgs &b, uint8_t *wsp, cudaStream_t st) {
     auto kern = linear_grad_kernel<DK, DVT>;
     e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(slots_of(a) * a.H), NT, smem, st>>>(b, ws);
-    e = cudaGetLastError();
+    e = launch_next(kern, dim3((unsigned)(slots_of(a) * a.H)), NT, smem, st, b, ws);
     if (e != cudaSuccess || !b.dg || a.decay != KDN_DECAY_HEAD) return e;
     return launch_linear_head_decay(a, ws.dgc, b.dg, C, st);
 }

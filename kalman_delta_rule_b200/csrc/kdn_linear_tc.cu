@@ -75,10 +75,6 @@ struct StateArgs {
     CUtensorMap tx, ty;
 };
 
-// The decay launch before this one is complete.  Every CTA waits for it, one without work too: what the stream runs
-// next must not start with the decay launch still under way because no CTA of this one had anything to do.
-__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // 32 columns of row `row` of a state, in pairs: from the caller's [dk, dv] layout (zero outside it) ...
 __device__ __forceinline__ void load_caller(f32x2 (&S)[16], const float *src, int dk, int dv, int row, int col) {
 #pragma unroll
@@ -133,7 +129,7 @@ __device__ __forceinline__ void add_delta(f32x2 (&S)[16], uint32_t d, float2 dec
 // a warp per (chunk, head), four tokens per lane
 __global__ void __launch_bounds__(256) linear_decay_kernel(LinArgs a, Decay *rec, long long n)
 {
-    asm volatile("griddepcontrol.launch_dependents;");   // the walk that follows may set itself up meanwhile
+    let_next_launch();                        // the walk that follows may set itself up meanwhile
     const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (id >= n) return;
@@ -721,17 +717,9 @@ cudaError_t setup(K kern, size_t smem, int threads) {
 // its records, and touch nothing else that it does)
 template <typename K, typename A>
 cudaError_t launch(K kern, long long grid, int threads, size_t smem, const A &args, bool early, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, args);
+    if (early) return launch_next(kern, dim3((unsigned)grid), threads, smem, st, args);
+    kern<<<(unsigned)grid, threads, smem, st>>>(args);
+    return cudaGetLastError();
 }
 
 template <bool REV, bool TOTALS>
