@@ -7,9 +7,11 @@
 // the variance is the mean of squared deviations from a mean that is already known.  LPR <= 32: a row
 // per part of a warp, sums by shuffles; LPR >= 128: a row per CTA.  All sums are fp32.
 // Both directions are bound by HBM: the forward moves 2 d elements per row, the backward 3 d.  A row's
-// reductions are a chain of latencies, so the next row's loads are issued before them; its arithmetic is packed
+// reductions are a chain of latencies, so the next rows' loads are issued before them; its arithmetic is packed
 // (two fp32 per instruction: with one, issue bounds the kernels before HBM does); and the launch has as
-// many CTAs as are resident at once (a second, partial wave cost up to a third).
+// many CTAs as are resident at once (a second, partial wave cost up to a third).  bf16: 16384 x 16 rows of 128
+// take 26.9 us (5.1 TB/s), their gradient 39.0 (5.2); the gradient of 16384 rows of 4096 87.7 (4.6), of which the sums
+// of the CTAs' shares of dw and db 7.
 //
 // dw and db: a row's threads always own the same columns of the same group, so each keeps its columns'
 // two sums in registers over all the rows it walks; the CTA's rows join in shared memory, and the CTA
@@ -76,6 +78,88 @@ struct Shape {
     static constexpr int FWD = NT >= 768 ? 1 : 768 / NT, BWD = NT >= 512 ? 1 : 512 / NT;
 };
 
+// A thread's rows on their way: NA arrays' elements of its columns and NS fp32 values per row.  Rows within a warp are
+// copied in 16-byte pieces to slots of the thread's own in shared memory, DEPTH rows ahead, which costs no registers and, as
+// no other thread reads them, no barrier (16384 x 16 rows of 128: 28.7 -> 26.9 us, the gradient 42.9 -> 39.1).  Rows over
+// a CTA, and single elements (odd widths), wait in registers, one row ahead: there a barrier per row sets the pace, and
+// the detour costs more than it brings (gradient of 16384 x 4096: 88 us, through shared memory 91).
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {   // (zeros where there is no element)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+template <typename T, int VEC, int LPR, int EPL, int NA, int NS>
+struct Ahead {
+    static constexpr bool ASYNC = VEC > 1 && LPR <= 32;
+    static constexpr int NT = Shape<LPR>::NT, NV = EPL / VEC, ROW = NT * (NA * NV * 16 + NS * 4);
+    static constexpr int ROOM = 110 * 1024 / ROW;          // two CTAs per SM
+    static constexpr int DEPTH = !ASYNC ? 1 : ROOM < 4 ? ROOM : 4;
+    static constexpr size_t BYTES = ASYNC ? (size_t)DEPTH * ROW : 0;
+    static_assert(DEPTH >= 1, "shared memory");
+    typedef typename Raw<T, VEC>::type raw_t;
+    uint8_t *mem;
+    int turn = 0;
+    raw_t raw[ASYNC ? 1 : NA * NV] = {};
+    float val[ASYNC || NS == 0 ? 1 : NS] = {};
+
+    __device__ __forceinline__ uint4 *piece(int st, int k) const { return reinterpret_cast<uint4 *>(mem) + (st * NA * NV + k) * NT + threadIdx.x; }
+    __device__ __forceinline__ float *value(int st, int k) const {
+        return reinterpret_cast<float *>(mem + (size_t)DEPTH * NA * NV * NT * 16) + (st * NS + k) * NT + threadIdx.x;
+    }
+    // row `row` of the arrays, if it is there; zeros where there is no row or no element
+    __device__ __forceinline__ void fetch(const void *const (&arr)[NA], const float *const (&vals)[NS > 0 ? NS : 1], size_t row, int d, int lane, bool there) {
+        if constexpr (ASYNC) {
+#pragma unroll
+            for (int n = 0; n < NA; ++n) {
+                const T *base = static_cast<const T *>(arr[n]) + (there ? row * d : 0);
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = (j * LPR + lane) * VEC;
+                    copy16(piece(turn, n * NV + j), there && c < d ? base + c : base, there && c < d);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NS; ++n) copy4(value(turn, n), vals[n] + (there ? row : 0), there);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (++turn == DEPTH) turn = 0;
+        } else {
+            if (!there) {
+#pragma unroll
+                for (int k = 0; k < NA * NV; ++k) raw[k] = raw_t();
+#pragma unroll
+                for (int n = 0; n < NS; ++n) val[n] = 0.f;
+                return;
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * LPR + lane) * VEC;
+                if (c >= d) continue;
+#pragma unroll
+                for (int n = 0; n < NA; ++n) raw[n * NV + j] = load_raw<T, VEC>(static_cast<const T *>(arr[n]) + row * d + c);
+            }
+#pragma unroll
+            for (int n = 0; n < NS; ++n) val[n] = __ldg(vals[n] + row);
+        }
+    }
+    // the row fetched DEPTH calls ago
+    __device__ __forceinline__ void take(float (&x)[NA][EPL], float (&v)[NS > 0 ? NS : 1]) {
+        if constexpr (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+#pragma unroll
+        for (int n = 0; n < NA; ++n)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if constexpr (ASYNC) widen<T, VEC>(x[n] + j * VEC, *piece(turn, n * NV + j));
+                else widen<T, VEC>(x[n] + j * VEC, raw[n * NV + j]);
+            }
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            if constexpr (ASYNC) v[n] = *value(turn, n);
+            else v[n] = val[n];
+        }
+    }
+};
+
 // N sums over the LPR threads of a row; every one of them gets them.  Over a CTA: one barrier, on two buffers in
 // turn (who writes a buffer again has passed a barrier that its readers reached after reading)
 template <int LPR, int N>
@@ -118,7 +202,6 @@ template <typename T, int VEC, int LPR, int EPL>
 __global__ void __launch_bounds__(Shape<LPR>::NT, Shape<LPR>::FWD) norm_kernel(NormArgs a)
 {
     constexpr int NV = EPL / VEC;
-    typedef typename Raw<T, VEC>::type raw_t;
     __shared__ float red[2][1][LPR > 32 ? LPR / 32 : 1];
     RowSum<LPR, 1> sum{red};
     const int g = blockIdx.x % a.G, lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
@@ -134,22 +217,18 @@ __global__ void __launch_bounds__(Shape<LPR>::NT, Shape<LPR>::FWD) norm_kernel(N
         w[e / 2] = pk2(param(a.weight, e, 1.f), param(a.weight, e + 1, 1.f));
         b[e / 2] = pk2(param(a.bias, e, 0.f), param(a.bias, e + 1, 0.f));
     }
-    raw_t next[NV] = {};
-    auto fetch = [&](long long i0) {
-        const long long i = i0 + sub;
-        if (i >= a.n) return;
-        const T *x = static_cast<const T *>(a.x) + ((size_t)i * a.G + g) * a.d;
+    extern __shared__ __align__(16) uint8_t mem[];
+    typedef Ahead<T, VEC, LPR, EPL, 1, 0> Next;
+    Next next{mem};
+    auto fetch = [&](long long i0) { next.fetch({a.x}, {nullptr}, (size_t)(i0 + sub) * a.G + g, a.d, lane, i0 + sub < a.n); };
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if ((j * LPR + lane) * VEC < a.d) next[j] = load_raw<T, VEC>(x + (j * LPR + lane) * VEC);
-    };
-    fetch(rows.first);
+    for (int k = 0; k < Next::DEPTH; ++k) fetch(rows.first + k * rows.step);
     for (long long i0 = rows.first; i0 < a.n; i0 += rows.step) {
         const long long i = i0 + sub;
-        float v[EPL], s[1];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) widen<T, VEC>(v + j * VEC, next[j]);   // (zero behind the row's end)
-        fetch(i0 + rows.step);
+        float vs[1][EPL], none[1], s[1];
+        next.take(vs, none);               // (zero behind the row's end)
+        fetch(i0 + Next::DEPTH * rows.step);
+        const float (&v)[EPL] = vs[0];
         f32x2 x[EPL / 2], s2 = 0;
 #pragma unroll
         for (int e = 0; e < EPL / 2; ++e) {
@@ -199,7 +278,6 @@ template <typename T, int VEC, int LPR, int EPL>
 __global__ void __launch_bounds__(Shape<LPR>::NT, Shape<LPR>::BWD) norm_backward_kernel(NormArgs a)
 {
     constexpr int ROWS = Shape<LPR>::ROWS, NV = EPL / VEC;
-    typedef typename Raw<T, VEC>::type raw_t;
     __shared__ float red[2][2][LPR > 32 ? LPR / 32 : 1];
     __shared__ float join[ROWS > 1 ? ROWS : 1][ROWS > 1 ? LPR * VEC : 1];
     RowSum<LPR, 2> sum{red};
@@ -217,39 +295,21 @@ __global__ void __launch_bounds__(Shape<LPR>::NT, Shape<LPR>::BWD) norm_backward
         dw[e] = db[e] = 0;
     }
     // a place without an element or a row holds zeros: dy's make every term of it vanish
-    raw_t next_x[NV] = {}, next_dy[NV] = {};
-    float next_mean = 0.f, next_rstd = 0.f;
+    extern __shared__ __align__(16) uint8_t mem[];
+    typedef Ahead<T, VEC, LPR, EPL, 2, 2> Next;
+    Next next{mem};
     auto fetch = [&](long long i0) {
-        const long long i = i0 + sub;
-        if (i >= a.n) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) next_x[j] = next_dy[j] = raw_t();
-            next_mean = next_rstd = 0.f;
-            return;
-        }
-        const size_t row = (size_t)i * a.G + g;
-        const T *x = static_cast<const T *>(a.x) + row * a.d, *dy = static_cast<const T *>(a.dy) + row * a.d;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + lane) * VEC;
-            if (c >= a.d) continue;
-            next_x[j] = load_raw<T, VEC>(x + c);
-            next_dy[j] = load_raw<T, VEC>(dy + c);
-        }
-        next_mean = __ldg(a.mean + row);
-        next_rstd = __ldg(a.rstd + row);
+        next.fetch({a.x, a.dy}, {a.mean, a.rstd}, (size_t)(i0 + sub) * a.G + g, a.d, lane, i0 + sub < a.n);
     };
-    fetch(rows.first);
+#pragma unroll
+    for (int k = 0; k < Next::DEPTH; ++k) fetch(rows.first + k * rows.step);
     for (long long i0 = rows.first; i0 < a.n; i0 += rows.step) {
         const long long i = i0 + sub;
-        float vx[EPL], vy[EPL], s[2];
-        const f32x2 mean2 = pk2(next_mean, next_mean), rstd2 = pk2(next_rstd, next_rstd);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            widen<T, VEC>(vx + j * VEC, next_x[j]);
-            widen<T, VEC>(vy + j * VEC, next_dy[j]);
-        }
-        fetch(i0 + rows.step);
+        float in[2][EPL], stat[2], s[2];
+        next.take(in, stat);
+        fetch(i0 + Next::DEPTH * rows.step);
+        const float (&vx)[EPL] = in[0], (&vy)[EPL] = in[1];
+        const f32x2 mean2 = pk2(stat[0], stat[0]), rstd2 = pk2(stat[1], stat[1]);
         f32x2 xh[EPL / 2], u[EPL / 2], s1 = 0, s2 = 0;
 #pragma unroll
         for (int e = 0; e < EPL / 2; ++e) {
@@ -312,38 +372,33 @@ __global__ void __launch_bounds__(Shape<LPR>::NT, Shape<LPR>::BWD) norm_backward
     }
 }
 
-// dw, db [G, d] from the CTAs' shares: thread = (column, one of 32 parts of the CTAs)
+// dw (blockIdx.z = 0) and db (1) [G, d] from the CTAs' shares: thread = (column, one of 32 parts of the CTAs)
 __global__ void __launch_bounds__(1024) norm_params_kernel(NormArgs a, int blocks)
 {
-    __shared__ float red[2][32][33];
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // (launched while the rows' kernel runs out)
+    __shared__ float red[32][33];
     const int g = blockIdx.y, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, part = threadIdx.x >> 5;
-    float s0 = 0.f, s1 = 0.f;
+    float *out = blockIdx.z ? a.dbias : a.dweight;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // (launched while the rows' kernel runs out)
+    if (!out) return;
+    float s = 0.f;
     if (c < a.d) {
-#pragma unroll 4
-        for (int b = g + part * a.G; b < blocks; b += 32 * a.G) {
-            s0 += __ldg(a.part + (size_t)b * 2 * a.d + c);
-            s1 += __ldg(a.part + (size_t)b * 2 * a.d + a.d + c);
-        }
+        const float *p = a.part + (size_t)blockIdx.z * a.d + c;
+#pragma unroll 8
+        for (int b = g + part * a.G; b < blocks; b += 32 * a.G) s += __ldg(p + (size_t)b * 2 * a.d);
     }
-    red[0][part][lane] = s0;
-    red[1][part][lane] = s1;
+    red[part][lane] = s;
     __syncthreads();
     // warp w joins the parts of column w
-    s0 = warp_sum(red[0][lane][part]);
-    s1 = warp_sum(red[1][lane][part]);
+    s = warp_sum(red[lane][part]);
     const int cw = blockIdx.x * 32 + part;
-    if (lane == 0 && cw < a.d) {
-        if (a.dweight) a.dweight[(size_t)g * a.d + cw] = s0;
-        if (a.dbias) a.dbias[(size_t)g * a.d + cw] = s1;
-    }
+    if (lane == 0 && cw < a.d) out[(size_t)g * a.d + cw] = s;
 }
 
 // CTAs of a launch: as many as are resident at once, a multiple of the groups, no more than the rows need
 template <typename K>
-cudaError_t blocks_for(K kern, int threads, const NormArgs &a, int rows, int *blocks) {
+cudaError_t blocks_for(K kern, size_t smem, int threads, const NormArgs &a, int rows, int *blocks) {
     KernelSetup ks;
-    const cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), 0, threads, false, &ks);
+    const cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), smem, threads, false, &ks);
     if (e != cudaSuccess) return e;
     long long per = (long long)ks.sms * ks.blocks_per_sm;
     if (per > kMaxBlocks) per = kMaxBlocks;
@@ -359,13 +414,14 @@ cudaError_t run(const NormArgs &a, bool back, cudaStream_t st) {
     using Sh = Shape<LPR>;
     int blocks = 0;
     auto kern = back ? norm_backward_kernel<T, VEC, LPR, EPL> : norm_kernel<T, VEC, LPR, EPL>;
-    cudaError_t e = blocks_for(kern, Sh::NT, a, Sh::ROWS, &blocks);
+    const size_t smem = back ? Ahead<T, VEC, LPR, EPL, 2, 2>::BYTES : Ahead<T, VEC, LPR, EPL, 1, 0>::BYTES;
+    cudaError_t e = blocks_for(kern, smem, Sh::NT, a, Sh::ROWS, &blocks);
     if (e != cudaSuccess) return e;
-    kern<<<blocks, Sh::NT, 0, st>>>(a);
+    kern<<<blocks, Sh::NT, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || !back || !a.part) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.d + 31) / 32, a.G);
+    cfg.gridDim = dim3((a.d + 31) / 32, a.G, 2);
     cfg.blockDim = dim3(1024);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
