@@ -4,7 +4,10 @@ The raw functions keep the C names (``kdn_forward_chunkwise``, ``kdn_decode_step
 ``kdn_gain_scan``, ``kdn_backward``, ``kdn_workspace_size``, ``kdn_last_device_error``,
 ``kdn_status_string``, ``kdn_version``) and take plain integers for pointers.
 ``forward``, ``backward``, ``decode_step`` and ``gain_scan`` marshal torch CUDA tensors into those
-calls: they allocate outputs and workspace with torch and pass the current stream.
+calls: they allocate outputs and workspace with torch and pass the current stream.  So do
+``linear_forward``, ``linear_backward``, ``linear_decode_step`` and ``linear_decode_tokens`` (linear
+attention with a decay for each head) and ``layer_norm`` and ``layer_norm_backward``, whose common call
+goes through the extension module ``_kdn_marshal.so`` instead of ctypes.
 Every step of the computation runs in the library's kernels; there is no CPU or
 PyTorch fallback -- a missing library or device raises.
 """

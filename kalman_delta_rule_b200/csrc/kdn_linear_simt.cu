@@ -8,7 +8,11 @@
 //   grad   per (chunk, head): dq, dk, dv and the decay's gradient
 // The scan reads and writes each chunk's state once, which costs about the token tensors' own
 // traffic at d = 128, and in exchange no step but its multiply-add chain is serial: a problem of
-// few, long sequences fills the GPU as well as one of many short ones.
+// few, long sequences fills the GPU as well as one of many short ones.  The backward's two
+// directions share the first two launches; a launch starts while the one before runs out, with the
+// caller's rows read before its results are waited for.  256 tokens of 2 heads of 32: 14.3 us, three
+// launches' latency.  Gradient of 24 ragged sequences, 5003 tokens of 4 heads of 64: 102.6 us, bound by
+// the fp32 products of `grad` (1.4 waves of its 408 CTAs, two per SM by shared memory; 54% issue activity).
 #include "kdn_common.cuh"
 #include "kdn_launch.h"
 

@@ -11,9 +11,11 @@
 //   W (8)    V' = diag(e^{G_C - G}) V as three bf16 terms; scores (TMEM) -> decayed, masked, bf16 -> P (TMEM)
 //   S (8)    S <- e^{G_C} S + delta in registers (fp32), its bf16 copy for Q S
 //   O (4)    o = scale (OI + e^G OS)
-// What bounds it is one pass over q, k, v and o at HBM's rate; the MMAs take about 2050 cycles per chunk
-// and tile (scores 512, Q S 384, delta 896 -- its A operand is read from shared memory three times --,
-// P V 256), which is about what the chunk's bytes take at an SM's share of the bandwidth.
+// Its floor is one pass over q, k, v and o at HBM's rate.  The MMAs take about 1950 cycles per chunk and tile (scores
+// 512, Q S 384, delta 800 -- its A operand, K, meets three terms of the weighted rows in one product of 192 columns --, P V
+// 256), shared memory's reads for them and the warps' passes about 2900, and a chunk 3450: a role's own latencies (TMEM
+// loads, conversions, the fence before its mbarrier) do not overlap with themselves.  B4 H16 T4096 d128: 79 us, 3.0 TB/s with
+// the decays' launch; tensor pipe 38% active, DRAM 39%.  One CTA per SM; that problem's 128 chains leave 20 SMs idle.
 // Rounding: P and the copy of S that Q reads are bf16 (o itself is); the state never is -- its products
 // take three-term weighted rows and it stays in fp32 registers, so it keeps fp32's accuracy over any length.
 //

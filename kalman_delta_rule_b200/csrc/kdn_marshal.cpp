@@ -128,7 +128,7 @@ PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     Linear l;
     void *s0;
-    if (n != 10 || !l.read(a[0], a[1], a[2], a[3], a[4], a[6], 4) || !optional(a[5], at::kFloat, l.dev, l.states, &s0)) Py_RETURN_NONE;
+    if (n != 10 || !PyBool_Check(a[9]) || !l.read(a[0], a[1], a[2], a[3], a[4], a[6], 4) || !optional(a[5], at::kFloat, l.dev, l.states, &s0)) Py_RETURN_NONE;
     at::Tensor o, s;
     void *sp;
     if (!optional(a[8], at::kFloat, l.dev, l.states, &sp)) Py_RETURN_NONE;
@@ -136,7 +136,7 @@ PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (kdn.linear_workspace_size(&l.p, &need) != KDN_OK || !l.output(a[7], *l.v, &o)) Py_RETURN_NONE;
     if (a[8] != Py_None) {
         s = *tensor(a[8]);
-    } else if (PyObject_IsTrue(a[9]) == 1) {
+    } else if (a[9] == Py_True) {
         s = floats(l.states, l.dev);
         sp = s.data_ptr();
     }
@@ -156,7 +156,7 @@ PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *linear_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     Linear l;
-    if (n != 8 || !l.read(a[0], a[1], a[2], a[3], Py_None, a[5], (int)PyLong_AsLong(a[7]))) Py_RETURN_NONE;
+    if (n != 8 || !PyLong_Check(a[7]) || !l.read(a[0], a[1], a[2], a[3], Py_None, a[5], (int)PyLong_AsLong(a[7]))) Py_RETURN_NONE;
     const at::Tensor *S = tensor(a[4]);
     at::Tensor o;
     if (!S || !is(*S, at::kFloat, l.dev, l.states) || !l.output(a[6], *l.v, &o)) Py_RETURN_NONE;
@@ -180,7 +180,7 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     Linear l;
     void *s0, *ds;
-    if (n != 10 || !l.read(a[0], a[1], a[2], a[3], a[5], a[8], 4) || !optional(a[6], at::kFloat, l.dev, l.states, &s0) ||
+    if (n != 10 || !PyBool_Check(a[9]) || !l.read(a[0], a[1], a[2], a[3], a[5], a[8], 4) || !optional(a[6], at::kFloat, l.dev, l.states, &s0) ||
         !optional(a[7], at::kFloat, l.dev, l.states, &ds))
         Py_RETURN_NONE;
     const at::Tensor *d_o = tensor(a[4]);
@@ -190,7 +190,7 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     at::Tensor dq = at::empty(l.q->sizes(), l.q->options()), dk = at::empty(l.q->sizes(), l.q->options()),
                dv = at::empty(l.v->sizes(), l.v->options()), dg, dS0;
     if (l.g) dg = floats(tensor(a[3])->sizes(), l.dev);
-    if (PyObject_IsTrue(a[9]) == 1) dS0 = floats(l.states, l.dev);
+    if (a[9] == Py_True) dS0 = floats(l.states, l.dev);
     const at::Tensor ws = scratch(need, l.dev);
     if (kdn.linear_backward(&l.p, l.q->data_ptr(), l.k->data_ptr(), l.v->data_ptr(), static_cast<float *>(l.g), static_cast<float *>(s0),
                             d_o->data_ptr(), static_cast<float *>(ds), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),

@@ -159,3 +159,26 @@ def test_aliased_outputs(lib):
             a = [at(n) for n in range(8)]
             a[j] = a[i]
             assert B.kdn_layer_norm_backward(4, 2, 64, 1, *a, *ws) == B.KDN_ERR_INVALID_ARG, (i, j)
+
+
+def test_native_step_leaves_other_calls_alone(lib):
+    """The wrappers' extension module: built, and None for what is not its call (here: tensors off the GPU, None, numbers)."""
+    import importlib.util
+    import os
+
+    import torch
+    spec = importlib.util.spec_from_file_location("_kdn_marshal", os.path.join(B.PKG, "_kdn_marshal.so"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    x, w = torch.zeros((1, 2, 2, 32)), torch.zeros(32)
+    g, S = torch.zeros((1, 2, 2)), torch.zeros((1, 2, 32, 32))
+    assert m.linear_forward(x, x, x, g, None, None, 1.0, None, None, True) is None
+    assert m.linear_decode(x, x, x, g, S, 1.0, None, 4) is None and m.linear_decode(x, x, x, g, S, 1.0, None, 3) is None
+    assert m.linear_backward(x, x, x, g, x, None, None, None, 1.0, True) is None
+    assert m.layer_norm(x, w, w, 1e-5, None) is None and m.layer_norm_backward(x, x, w, g, g) is None
+    for f in (m.linear_forward, m.linear_decode, m.linear_backward, m.layer_norm, m.layer_norm_backward):
+        assert f() is None and f(1) is None and f(*[None] * 10) is None and f(*[None] * 5) is None and f(*[None] * 8) is None
+    with pytest.raises(TypeError):
+        m.bind(1, 2)
+    with pytest.raises(TypeError):
+        m.bind(*["x"] * 8)
