@@ -5,7 +5,7 @@
 //
 // A row is held in the registers of LPR threads, EPL elements each, so x (and dy) is read once and
 // the variance is the mean of squared deviations from a mean that is already known.  LPR <= 32: a row
-// per part of a warp, sums by shuffles; LPR >= 128: a row per CTA.  All sums are fp32.
+// per part of a warp, sums by shuffles; LPR >= 64: a row per CTA.  All sums are fp32.
 // Both directions are bound by HBM: the forward moves 2 d elements per row, the backward 3 d.  A row's
 // reductions are a chain of latencies, so the next rows' loads are issued before them; its arithmetic is packed
 // (two fp32 per instruction: with one, issue bounds the kernels before HBM does); and the launch has as
@@ -26,10 +26,11 @@ namespace {
 
 constexpr int kMaxBlocks = 148 * 8;   // CTAs of a launch (backward: shares of dw, db in the workspace)
 
-// VEC elements as they are in memory (16 bytes, or one element), and widened
+// VEC elements as they are in memory (16 bytes, a pair of bf16, or one element), and widened
 template <typename T, int VEC> struct Raw { typedef uint4 type; };
 template <> struct Raw<float, 1> { typedef float type; };
 template <> struct Raw<bf16, 1> { typedef unsigned short type; };
+template <> struct Raw<bf16, 2> { typedef unsigned type; };
 template <typename T, int VEC>
 __device__ __forceinline__ typename Raw<T, VEC>::type load_raw(const T *src) {
     return __ldg(reinterpret_cast<const typename Raw<T, VEC>::type *>(src));
@@ -46,6 +47,9 @@ __device__ __forceinline__ void widen(float *dst, const typename Raw<T, VEC>::ty
     } else if constexpr (VEC == 4) {
         dst[0] = __uint_as_float(u.x); dst[1] = __uint_as_float(u.y);
         dst[2] = __uint_as_float(u.z); dst[3] = __uint_as_float(u.w);
+    } else if constexpr (VEC == 2) {
+        dst[0] = __uint_as_float(u << 16);
+        dst[1] = __uint_as_float(u & 0xffff0000u);
     } else if constexpr (sizeof(T) == 4) {
         dst[0] = u;
     } else {
@@ -65,6 +69,8 @@ __device__ __forceinline__ void store_vec(T *dst, const float *src) {
         *reinterpret_cast<uint4 *>(dst) = u;
     } else if constexpr (VEC == 4) {
         stf4(dst, make_float4(src[0], src[1], src[2], src[3]));
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(src[0], src[1]);
     } else {
         stf(dst, src[0]);
     }
@@ -79,9 +85,9 @@ struct Shape {
 };
 
 // A thread's rows on their way: NA arrays' elements of its columns and NS fp32 values per row.  Rows within a warp are
-// copied in 16-byte pieces to slots of the thread's own in shared memory, DEPTH rows ahead, which costs no registers and, as
+// copied, if in 16-byte pieces, to slots of the thread's own in shared memory, DEPTH rows ahead, which costs no registers and, as
 // no other thread reads them, no barrier (16384 x 16 rows of 128: 28.7 -> 26.9 us, the gradient 42.9 -> 39.1).  Rows over
-// a CTA, and single elements (odd widths), wait in registers, one row ahead: there a barrier per row sets the pace, and
+// a CTA, and pieces of other sizes, wait in registers, one row ahead: there a barrier per row sets the pace, and
 // the detour costs more than it brings (gradient of 16384 x 4096: 88 us, through shared memory 91).
 __device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {   // (zeros where there is no element)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -91,7 +97,7 @@ __device__ __forceinline__ void copy4(void *dst, const void *src, bool there) {
 }
 template <typename T, int VEC, int LPR, int EPL, int NA, int NS>
 struct Ahead {
-    static constexpr bool ASYNC = VEC > 1 && LPR <= 32;
+    static constexpr bool ASYNC = VEC * sizeof(T) == 16 && LPR <= 32;
     static constexpr int NT = Shape<LPR>::NT, NV = EPL / VEC, ROW = NT * (NA * NV * 16 + NS * 4);
     static constexpr int ROOM = 110 * 1024 / ROW;          // two CTAs per SM
     static constexpr int DEPTH = !ASYNC ? 1 : ROOM < 4 ? ROOM : 4;
@@ -433,22 +439,29 @@ cudaError_t run(const NormArgs &a, bool back, cudaStream_t st) {
 }
 
 // Within a warp 16 elements per thread (8 for the narrowest rows): against 8, a row of 128 costs a quarter fewer
-// instructions, which is what bounds short rows.  Across a CTA the rows in flight per SM count: the smallest CTA
-// whose backward (five values per element) still leaves room for a second one.
+// instructions, which is what bounds short rows.  Across a CTA the rows in flight per SM count, so CTAs are small: 16
+// elements per thread against 8 bring rows of 2048 bf16 from 21.6 to 15.9 us (10000 of them; gradient of 15000 x 1602 from
+// 65 to 43).  Odd widths, an element per load, are bound by their instructions, and 8 per thread are quicker (20000 x 1001
+// bf16 24.7 us against 31.2).
 template <typename T, int VEC>
 cudaError_t by_width(const NormArgs &a, bool back, cudaStream_t st) {
     if (a.d <= 64) return run<T, VEC, 8, 8>(a, back, st);
     if (a.d <= 128) return run<T, VEC, 8, 16>(a, back, st);
     if (a.d <= 256) return run<T, VEC, 16, 16>(a, back, st);
     if (a.d <= 512) return run<T, VEC, 32, 16>(a, back, st);
-    if (a.d <= 1024) return run<T, VEC, 128, 8>(a, back, st);
-    if (a.d <= 2048) return run<T, VEC, 256, 8>(a, back, st);
+    constexpr int N = VEC > 1 ? 16 : 8;    // elements per thread
+    if (a.d <= 1024) return run<T, VEC, 1024 / N, N>(a, back, st);
+    if (a.d <= 2048) return run<T, VEC, 2048 / N, N>(a, back, st);
     if (a.d <= 4096) return run<T, VEC, 256, 16>(a, back, st);
     if (a.d <= 8192) return run<T, VEC, 512, 16>(a, back, st);
     return run<T, VEC, 1024, 16>(a, back, st);
 }
+// (bf16 rows of an even width in pairs: 50000 x 510 21.4 us, element by element 38.6)
 cudaError_t launch(const NormArgs &a, bool bf16_in, bool back, cudaStream_t st) {
-    if (bf16_in) return a.d % 8 == 0 ? by_width<bf16, 8>(a, back, st) : by_width<bf16, 1>(a, back, st);
+    if (bf16_in) {
+        if (a.d % 8 == 0) return by_width<bf16, 8>(a, back, st);
+        return a.d % 2 == 0 ? by_width<bf16, 2>(a, back, st) : by_width<bf16, 1>(a, back, st);
+    }
     return a.d % 4 == 0 ? by_width<float, 4>(a, back, st) : by_width<float, 1>(a, back, st);
 }
 

@@ -8,7 +8,8 @@ pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 # every width class: parts of a warp, a warp, a CTA of 256 and of 512 threads; vector and element loads
-WIDTHS = [1, 7, 32, 63, 64, 100, 128, 129, 256, 300, 512, 777, 1000, 1001, 1024, 1031, 2048, 2050, 4096, 4100, 8192, 8195, 16383, 16384]
+WIDTHS = [1, 7, 32, 63, 64, 100, 128, 129, 256, 300, 512, 777, 1000, 1001, 1024, 1031, 2048, 2050, 4096, 4100, 8192, 8195, 16383, 16384,
+          2, 6, 62, 126, 254, 510, 514, 1022, 1502, 4094, 8190, 12002]
 
 
 def make(seed, shape, dtype, G=None, affine=True, offset=0.5):
