@@ -227,8 +227,9 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(LinArgs a, Walks ws, c
 }
 
 // ------------------------------------------------------------------ out
-template <int DK, int DVT>
-__global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *S)
+// FOLD: of the chunks' own contributions each CTA forms its state itself, and a sequence's last one S_out: no scan.
+template <int DK, int DVT, bool FOLD>
+__global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *S, const float2 *dec)
 {
     extern __shared__ __align__(16) float sm[];
     float *Qs = sm, *Ks = Qs + C * (DK + PAD), *Vs = Ks + C * (DK + PAD), *Ss = Vs + C * (DVT + PAD),
@@ -237,13 +238,11 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
     const Log2 *G = dec_s.G;
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H, col = blockIdx.y * DVT;
     LinPiece p;
-    if (!lin_piece(a, u, C, p) || p.len == 0) return wait_for_launch();
+    if (!lin_piece(a, u, C, p) || (p.len == 0 && !FOLD)) return wait_for_launch();
     const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
     load_rows<DK>(Qs, a.q, tok, L, a.H, h, DK, 0);
     load_rows<DK>(Ks, a.k, tok, L, a.H, h, DK, 0);
     load_rows<DVT>(Vs, a.v, tok, L, a.H, h, a.dv, col);
-    wait_for_launch();                     // the states are complete
-    load_state<DK, DVT>(Ss, S + ((size_t)u * a.H + h) * DK * a.dv + col, a.dv);
     chunk_log_decay(a, tok, L, h, &dec_s);
     const float scale = a.scale * dec_s.one;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -257,6 +256,43 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
                 const int t = ty * 4 + i, s = tx + 16 * j;
                 Ps[t * (C + PAD) + s] = s <= t ? scale * acc[i][j] * lin_exp2_between(G[t], G[s]) : 0.f;
             }
+    }
+    wait_for_launch();                     // the states, or the contributions, are complete
+    const size_t slot = (size_t)u * a.H + h, per = (size_t)DK * a.dv;
+    if constexpr (FOLD) {
+        constexpr int N = DK * DVT / 4 / NT;
+        const size_t seq = ((size_t)p.s * a.H + h) * per + col;
+        size_t at[N];
+        float4 x[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int i = threadIdx.x + e * NT;
+            at[e] = (size_t)(i / (DVT / 4)) * a.dv + (i % (DVT / 4)) * 4;
+            x[e] = a.S0 ? ldf4(a.S0 + seq + at[e]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        auto add = [&](int c) {            // chunk c's contribution
+            const float2 f = dec[slot - (size_t)(p.j - c) * a.H];
+            const float *U = S + (slot - (size_t)(p.j - c) * a.H) * per + col;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float4 y = *reinterpret_cast<const float4 *>(U + at[e]);
+                x[e] = make_float4(lin_carry(f, x[e].x, y.x), lin_carry(f, x[e].y, y.y), lin_carry(f, x[e].z, y.z), lin_carry(f, x[e].w, y.w));
+            }
+        };
+#pragma unroll 2
+        for (int c = 0; c < p.j; ++c) add(c);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int i = threadIdx.x + e * NT;
+            *reinterpret_cast<float4 *>(Ss + (i / (DVT / 4)) * (DVT + PAD) + (i % (DVT / 4)) * 4) = x[e];
+        }
+        if (a.S_out && p.j * C + C >= p.len) {
+            if (L > 0) add(p.j);
+#pragma unroll
+            for (int e = 0; e < N; ++e) stf4(a.S_out + seq + at[e], x[e]);
+        }
+    } else {
+        load_state<DK, DVT>(Ss, S + slot * per + col, a.dv);
     }
     __syncthreads();
     float acc[4][DVT / 16] = {};
@@ -479,31 +515,45 @@ size_t head_bytes(const LinArgs &a) { return round256((size_t)slots_of(a) * a.H 
 
 // the first two steps for one direction or both
 template <int DK, int DVT>
-cudaError_t states(const LinArgs &a, const Walks &ws, int walks, float2 *dec, cudaStream_t st) {
+cudaError_t deltas(const LinArgs &a, const Walks &ws, int walks, float2 *dec, cudaStream_t st) {
     constexpr size_t smem = sizeof(float) * C * (DK + DVT + 2 * PAD);
     KernelSetup ks;
     auto kern = linear_delta_kernel<DK, DVT>;
-    cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
+    const cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
     if (e != cudaSuccess) return e;
     kern<<<dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT, walks), NT, smem, st>>>(a, ws, dec);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+cudaError_t scans(const LinArgs &a, const Walks &ws, int walks, const float2 *dec, cudaStream_t st) {
     const long long threads = (long long)a.nseq * a.H * (a.dk * a.dv / 4);
-    return launch_next(linear_scan_kernel, dim3((unsigned)((threads + 255) / 256), 1, walks), 256, 0, st, a, ws, (const float2 *)dec);
+    return launch_next(linear_scan_kernel, dim3((unsigned)((threads + 255) / 256), 1, walks), 256, 0, st, a, ws, dec);
+}
+
+// Sequences of at most FOLDED chunks go without the scan: its launch costs more than reading a few contributions
+// again does (256 tokens of 2 heads of 32: 14.4 -> 10.4 us; 512 of 1024 heads of 128, where most is read
+// again: 4032 -> 3592).
+constexpr int FOLDED = 8;
+
+template <int DK, int DVT, bool FOLD>
+cudaError_t outputs(const LinArgs &a, const float *U, const float2 *dec, cudaStream_t st) {
+    constexpr size_t smem = sizeof(float) * (C * (2 * DK + DVT + C + 4 * PAD) + DK * (DVT + PAD));
+    KernelSetup ks;
+    auto kern = linear_out_kernel<DK, DVT, FOLD>;
+    const cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
+    if (e != cudaSuccess) return e;
+    return launch_next(kern, dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT), NT, smem, st, a, U, dec);
 }
 
 template <int DK, int DVT>
 cudaError_t forward(const LinArgs &a, uint8_t *ws, cudaStream_t st) {
     float *U = reinterpret_cast<float *>(ws);
+    float2 *dec = reinterpret_cast<float2 *>(ws + state_bytes(a));
     const Walks wk{{{a.k, a.v, U, a.S0, a.S_out}, {}}};
-    cudaError_t e = states<DK, DVT>(a, wk, 1, reinterpret_cast<float2 *>(ws + state_bytes(a)), st);
+    cudaError_t e = deltas<DK, DVT>(a, wk, 1, dec, st);
     if (e != cudaSuccess) return e;
-    constexpr size_t smem = sizeof(float) * (C * (2 * DK + DVT + C + 4 * PAD) + DK * (DVT + PAD));
-    KernelSetup ks;
-    auto kern = linear_out_kernel<DK, DVT>;
-    e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
-    if (e != cudaSuccess) return e;
-    return launch_next(kern, dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT), NT, smem, st, a, (const float *)U);
+    if ((a.cu ? a.ntok : a.T) <= FOLDED * C) return outputs<DK, DVT, true>(a, U, dec, st);
+    e = scans(a, wk, 1, dec, st);
+    return e != cudaSuccess ? e : outputs<DK, DVT, false>(a, U, dec, st);
 }
 
 template <int DK, int DVT>
@@ -515,7 +565,8 @@ cudaError_t backward(const LinBwdArgs &b, uint8_t *wsp, cudaStream_t st) {
     ws.dec = reinterpret_cast<float2 *>(wsp + 2 * state_bytes(a));
     ws.dgc = reinterpret_cast<float *>(wsp + 2 * state_bytes(a) + head_bytes(a));
     const Walks wk{{{a.k, a.v, ws.U, a.S0, nullptr}, {a.q, b.d_o, ws.E, b.dS_T, b.dS0}}};
-    cudaError_t e = states<DK, DVT>(a, wk, 2, ws.dec, st);
+    cudaError_t e = deltas<DK, DVT>(a, wk, 2, ws.dec, st);
+    if (e == cudaSuccess) e = scans(a, wk, 2, ws.dec, st);
     if (e != cudaSuccess) return e;
     constexpr size_t smem = sizeof(float) * (C * (2 * DK + 2 * DVT + C + 5 * PAD) + DK * (DVT + PAD));
     KernelSetup ks;
