@@ -3,15 +3,16 @@
 //   delta  per (chunk, head, d_v tile): the chunk's own contribution U = K^T diag(w) V (w = decay to
 //          the chunk's end) or, for the gradient, E = scale Q^T diag(e^G) dO, and the chunk's decay
 //   scan   per state element: the contributions become the states at the chunks' starts
-//          (S <- decay S + U, forwards), or the state gradients at the chunks' ends (backwards)
+//          (S <- decay S + U, forwards), or the state gradients at the chunks' ends (backwards);
+//          left out for sequences of a few chunks, whose CTAs add up what they need themselves
 //   out    per (chunk, head, d_v tile): o
 //   grad   per (chunk, head): dq, dk, dv and the decay's gradient
 // The scan reads and writes each chunk's state once, which costs about the token tensors' own
 // traffic at d = 128, and in exchange no step but its multiply-add chain is serial: a problem of
 // few, long sequences fills the GPU as well as one of many short ones.  The backward's two
 // directions share the first two launches; a launch starts while the one before runs out, with the
-// caller's rows read before its results are waited for.  256 tokens of 2 heads of 32: 14.3 us, three
-// launches' latency.  Gradient of 24 ragged sequences, 5003 tokens of 4 heads of 64: 102.6 us, bound by
+// caller's rows read before its results are waited for.  256 tokens of 2 heads of 32: 10.4 us, two
+// launches' latency.  Gradient of 24 ragged sequences, 5003 tokens of 4 heads of 64: 97 us, bound by
 // the fp32 products of `grad` (1.4 waves of its 408 CTAs, two per SM by shared memory; 54% issue activity).
 #include "kdn_common.cuh"
 #include "kdn_launch.h"
@@ -116,6 +117,36 @@ __device__ __forceinline__ float row_sum(float x) {
     for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
+
+// A [DK][DVT] tile of a state (row stride dv) in the registers of a CTA, to which chunks' contributions are added.
+template <int DK, int DVT>
+struct Fold {
+    static constexpr int N = DK * DVT / 4 / NT;
+    float4 x[N];
+    static __device__ __forceinline__ size_t at(int e, int dv) {
+        const int i = threadIdx.x + e * NT;
+        return (size_t)(i / (DVT / 4)) * dv + (i % (DVT / 4)) * 4;
+    }
+    static __device__ __forceinline__ float4 *in(float *tile, int e) {        // its place in shared memory
+        const int i = threadIdx.x + e * NT;
+        return reinterpret_cast<float4 *>(tile + (i / (DVT / 4)) * (DVT + PAD) + (i % (DVT / 4)) * 4);
+    }
+    __device__ __forceinline__ void start(const float *p, size_t off, int dv) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = p ? ldf4(p + off + at(e, dv)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void add(float2 f, const float *U, int dv) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float4 y = *reinterpret_cast<const float4 *>(U + at(e, dv));
+            x[e] = make_float4(lin_carry(f, x[e].x, y.x), lin_carry(f, x[e].y, y.y), lin_carry(f, x[e].z, y.z), lin_carry(f, x[e].w, y.w));
+        }
+    }
+    __device__ __forceinline__ void store(float *p, int dv) const {
+#pragma unroll
+        for (int e = 0; e < N; ++e) stf4(p + at(e, dv), x[e]);
+    }
+};
 
 struct Ws {
     float *U, *E;              // [slots, H, dk, dv]: states at the chunks' starts; state gradients at their ends
@@ -260,36 +291,20 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
     wait_for_launch();                     // the states, or the contributions, are complete
     const size_t slot = (size_t)u * a.H + h, per = (size_t)DK * a.dv;
     if constexpr (FOLD) {
-        constexpr int N = DK * DVT / 4 / NT;
         const size_t seq = ((size_t)p.s * a.H + h) * per + col;
-        size_t at[N];
-        float4 x[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int i = threadIdx.x + e * NT;
-            at[e] = (size_t)(i / (DVT / 4)) * a.dv + (i % (DVT / 4)) * 4;
-            x[e] = a.S0 ? ldf4(a.S0 + seq + at[e]) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        Fold<DK, DVT> x;
+        x.start(a.S0, seq, a.dv);
         auto add = [&](int c) {            // chunk c's contribution
-            const float2 f = dec[slot - (size_t)(p.j - c) * a.H];
-            const float *U = S + (slot - (size_t)(p.j - c) * a.H) * per + col;
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float4 y = *reinterpret_cast<const float4 *>(U + at[e]);
-                x[e] = make_float4(lin_carry(f, x[e].x, y.x), lin_carry(f, x[e].y, y.y), lin_carry(f, x[e].z, y.z), lin_carry(f, x[e].w, y.w));
-            }
+            const size_t from = slot - (size_t)(p.j - c) * a.H;
+            x.add(dec[from], S + from * per + col, a.dv);
         };
 #pragma unroll 2
         for (int c = 0; c < p.j; ++c) add(c);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int i = threadIdx.x + e * NT;
-            *reinterpret_cast<float4 *>(Ss + (i / (DVT / 4)) * (DVT + PAD) + (i % (DVT / 4)) * 4) = x[e];
-        }
+        for (int e = 0; e < x.N; ++e) *x.in(Ss, e) = x.x[e];
         if (a.S_out && p.j * C + C >= p.len) {
             if (L > 0) add(p.j);
-#pragma unroll
-            for (int e = 0; e < N; ++e) stf4(a.S_out + seq + at[e], x[e]);
+            x.store(a.S_out + seq, a.dv);
         }
     } else {
         load_state<DK, DVT>(Ss, S + slot * per + col, a.dv);
@@ -321,7 +336,7 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
 //   dg_t = sum over pairs (query i >= t, key j < t), in the chunk, before and behind it:
 //        sum_{s >= t} (rows Z - columns Z)_s + sum_{s >= t} q_s.(a dO S^T)_s + sum_{s < t} k_s.(w V R^T)_s + e^{G_C} <S, R>
 // No term is divided by a decay, and none of the four cancels against another.
-template <int DK, int DVT>
+template <int DK, int DVT, bool FOLD>
 __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
 {
     const LinArgs &a = b.a;
@@ -335,7 +350,14 @@ __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBw
     __shared__ float zr[C], zc[8][C], xi[C], yi[C], wsum[8];
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H;
     LinPiece p;
-    if (!lin_piece(a, u, C, p) || p.len == 0) return wait_for_launch();
+    if (!lin_piece(a, u, C, p)) return wait_for_launch();
+    const size_t seq = ((size_t)p.s * a.H + h) * DK * a.dv;
+    if (p.len == 0) {
+        if (FOLD && b.dS0)
+            for (int e = threadIdx.x * 4; e < DK * a.dv; e += NT * 4)
+                stf4(b.dS0 + seq + e, b.dS_T ? ldf4(b.dS_T + seq + e) : make_float4(0.f, 0.f, 0.f, 0.f));
+        return wait_for_launch();
+    }
     const int tok = p.t0 + p.j * C, L = min(C, p.len - p.j * C);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const size_t sbase = ((size_t)u * a.H + h) * DK * a.dv;
@@ -362,17 +384,45 @@ __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBw
         __syncthreads();       // the previous tile is read; Ps is written
         load_rows<DVT>(Vs, a.v, tok, L, a.H, h, a.dv, col);
         load_rows<DVT>(Os, b.d_o, tok, L, a.H, h, a.dv, col);
-        load_state<DK, DVT>(Ss, ws.U + sbase + col, a.dv);
+        // chunk c's slot is slot + (c - j) H
+        const size_t slot = (size_t)u * a.H + h, per = (size_t)DK * a.dv;
+        if constexpr (FOLD) {
+            Fold<DK, DVT> x;
+            x.start(a.S0, seq + col, a.dv);
+#pragma unroll 2
+            for (int c = p.j; c > 0; --c) x.add(ws.dec[slot - (size_t)c * a.H], ws.U + (slot - (size_t)c * a.H) * per + col, a.dv);
+#pragma unroll
+            for (int e = 0; e < x.N; ++e) *x.in(Ss, e) = x.x[e];
+        } else {
+            load_state<DK, DVT>(Ss, ws.U + sbase + col, a.dv);
+        }
         __syncthreads();
         mm<4, false, true>(dp, Os, DVT + PAD, Vs, DVT + PAD, DVT, ty, tx);
         mm<NK, false, true>(dqi, Os, DVT + PAD, Ss, DVT + PAD, DVT, ty, tx);
         __syncthreads();
-        for (int i = threadIdx.x; i < DK * (DVT / 4); i += NT) {   // R over S, and their inner product
-            const int r = i / (DVT / 4), c = (i % (DVT / 4)) * 4;
-            float4 *at = reinterpret_cast<float4 *>(Ss + r * (DVT + PAD) + c);
-            const float4 x = *at, y = *reinterpret_cast<const float4 *>(ws.E + sbase + col + (size_t)r * a.dv + c);
-            sr = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, sr))));
-            *at = y;
+        if constexpr (FOLD) {                                      // R over S, and their inner product
+            Fold<DK, DVT> y;
+            y.start(b.dS_T, seq + col, a.dv);
+#pragma unroll 2
+            for (int c = (p.len - 1) / C - p.j; c > 0; --c) y.add(ws.dec[slot + (size_t)c * a.H], ws.E + (slot + (size_t)c * a.H) * per + col, a.dv);
+#pragma unroll
+            for (int e = 0; e < y.N; ++e) {
+                float4 *at = y.in(Ss, e);
+                sr = fmaf(at->x, y.x[e].x, fmaf(at->y, y.x[e].y, fmaf(at->z, y.x[e].z, fmaf(at->w, y.x[e].w, sr))));
+                *at = y.x[e];
+            }
+            if (b.dS0 && p.j == 0) {
+                y.add(ws.dec[slot], ws.E + slot * per + col, a.dv);
+                y.store(b.dS0 + seq + col, a.dv);
+            }
+        } else {
+            for (int i = threadIdx.x; i < DK * (DVT / 4); i += NT) {
+                const int r = i / (DVT / 4), c = (i % (DVT / 4)) * 4;
+                float4 *at = reinterpret_cast<float4 *>(Ss + r * (DVT + PAD) + c);
+                const float4 x = *at, y = *reinterpret_cast<const float4 *>(ws.E + sbase + col + (size_t)r * a.dv + c);
+                sr = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, sr))));
+                *at = y;
+            }
         }
         __syncthreads();
         mm<NK, false, true>(dki, Vs, DVT + PAD, Rs, DVT + PAD, DVT, ty, tx);
@@ -529,10 +579,14 @@ cudaError_t scans(const LinArgs &a, const Walks &ws, int walks, const float2 *de
     return launch_next(linear_scan_kernel, dim3((unsigned)((threads + 255) / 256), 1, walks), 256, 0, st, a, ws, dec);
 }
 
-// Sequences of at most FOLDED chunks go without the scan: its launch costs more than reading a few contributions
-// again does (256 tokens of 2 heads of 32: 14.4 -> 10.4 us; 512 of 1024 heads of 128, where most is read
-// again: 4032 -> 3592).
-constexpr int FOLDED = 8;
+// Sequences of a few chunks go without the scan: its launch costs more than reading their contributions again does (256
+// tokens of 2 heads of 32: 14.4 -> 10.4 us; 512 of 1024 heads of 128, where most is read again: 4032 -> 3592; the gradient
+// of 5003 tokens in 24 sequences, H4 d64: 102 -> 97).  Packed lengths are known on the device only: a few chunks on
+// average, and not so many tokens in all that a single sequence of them would matter.
+bool folded(const LinArgs &a) {
+    constexpr int FEW = 8 * C;
+    return a.cu ? a.ntok <= FEW || (a.ntok <= 16 * FEW && a.ntok / FEW < a.nseq) : a.T <= FEW;
+}
 
 template <int DK, int DVT, bool FOLD>
 cudaError_t outputs(const LinArgs &a, const float *U, const float2 *dec, cudaStream_t st) {
@@ -551,7 +605,7 @@ cudaError_t forward(const LinArgs &a, uint8_t *ws, cudaStream_t st) {
     const Walks wk{{{a.k, a.v, U, a.S0, a.S_out}, {}}};
     cudaError_t e = deltas<DK, DVT>(a, wk, 1, dec, st);
     if (e != cudaSuccess) return e;
-    if ((a.cu ? a.ntok : a.T) <= FOLDED * C) return outputs<DK, DVT, true>(a, U, dec, st);
+    if (folded(a)) return outputs<DK, DVT, true>(a, U, dec, st);
     e = scans(a, wk, 1, dec, st);
     return e != cudaSuccess ? e : outputs<DK, DVT, false>(a, U, dec, st);
 }
@@ -566,11 +620,12 @@ cudaError_t backward(const LinBwdArgs &b, uint8_t *wsp, cudaStream_t st) {
     ws.dgc = reinterpret_cast<float *>(wsp + 2 * state_bytes(a) + head_bytes(a));
     const Walks wk{{{a.k, a.v, ws.U, a.S0, nullptr}, {a.q, b.d_o, ws.E, b.dS_T, b.dS0}}};
     cudaError_t e = deltas<DK, DVT>(a, wk, 2, ws.dec, st);
-    if (e == cudaSuccess) e = scans(a, wk, 2, ws.dec, st);
+    const bool fold = folded(a);
+    if (e == cudaSuccess && !fold) e = scans(a, wk, 2, ws.dec, st);
     if (e != cudaSuccess) return e;
     constexpr size_t smem = sizeof(float) * (C * (2 * DK + 2 * DVT + C + 5 * PAD) + DK * (DVT + PAD));
     KernelSetup ks;
-    auto kern = linear_grad_kernel<DK, DVT>;
+    auto kern = fold ? linear_grad_kernel<DK, DVT, true> : linear_grad_kernel<DK, DVT, false>;
     e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
     if (e != cudaSuccess) return e;
     e = launch_next(kern, dim3((unsigned)(slots_of(a) * a.H)), NT, smem, st, b, ws);
