@@ -355,7 +355,7 @@ def test_refusals(kdn):
 # totals of the earlier ones; fp32 ones are scanned, but for those of a few chunks (packed: on average).
 LONG = [(1, 2304, 1, 128, 128, None), (2, 4100, 1, 64, 64, None), (1, 3400, 2, 32, 256, [1, 3000, 0, 399]),
         (1, 2600, 1, 128, 256, [2600]), (1, 2500, 3, 128, 64, [0, 2499, 1]), (1, 2410, 1, 64, 64, [1000, 1010, 400]),
-        (1, 1510, 2, 64, 128, [0, 700, 3, 64, 65, 128, 129, 200, 1, 210])]
+        (1, 1500, 2, 64, 128, [0, 700, 3, 64, 65, 128, 129, 200, 1, 210])]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
