@@ -12,7 +12,7 @@
 // few, long sequences fills the GPU as well as one of many short ones.  The backward's two
 // directions share the first two launches; a launch starts while the one before runs out, with the
 // caller's rows read before its results are waited for.  256 tokens of 2 heads of 32: 10.4 us, two
-// launches' latency.  Gradient of 24 ragged sequences, 5003 tokens of 4 heads of 64: 97 us, bound by
+// launches' latency.  Gradient of 24 ragged sequences, 5003 tokens of 4 heads of 64: 97-101 us, bound by
 // the fp32 products of `grad` (1.4 waves of its 408 CTAs, two per SM by shared memory; 54% issue activity).
 #include "kdn_common.cuh"
 #include "kdn_launch.h"
