@@ -380,7 +380,7 @@ def gain_scan(k, alpha, sigma, r, cu_seqlens=None, P0=None, mu: float = 1.0, chu
 # These wrappers serve single-token decoding too, where the kernel takes a few microseconds.  The common call --
 # contiguous tensors of the expected types and shapes on the current device, its current stream, no caller's workspace --
 # goes from the tensors to the C ABI in one native step (csrc/kdn_marshal.cpp).  For any other that returns None, and
-# the code here checks, dispatches and raises.
+# the code here checks, dispatches and raises.  (A call that the library began and failed in raises there.)
 _native_mod = None
 _mod = None
 _raw_stream = None   # device index -> handle of its current stream
@@ -414,6 +414,7 @@ def _native():
         names = ("linear_workspace_size", "linear_forward", "linear_decode_tokens", "linear_backward_workspace_size",
                  "linear_backward", "layer_norm", "layer_norm_backward_workspace_size", "layer_norm_backward")
         mod.bind(*(ctypes.cast(getattr(lib, "kdn_" + n), _vp).value for n in names))
+        mod.raise_with(KdnError)
         _native_mod = mod
     return _native_mod
 

@@ -123,8 +123,10 @@ __device__ __forceinline__ float lin_carry(float2 decay, float s, float u) { ret
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// (The status is the launch's own: cudaGetLastError() after <<< >>> may be that of an earlier call, and a decode step reported
+// as failed has taken its token all the same.)
 template <typename... P, typename... A>
-cudaError_t launch_next(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+cudaError_t launch_with(bool early, void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
@@ -134,8 +136,18 @@ cudaError_t launch_next(void (*kern)(P...), dim3 grid, int threads, size_t smem,
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+// a call's first launch, or one that starts when the launch before is done ...
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+    return launch_with(false, kern, grid, threads, smem, st, args...);
+}
+// ... and one that follows programmatically
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+    return launch_with(true, kern, grid, threads, smem, st, args...);
 }
 
 }  // namespace kdn

@@ -27,7 +27,11 @@ bool distinct(std::initializer_list<const void *> outs, std::initializer_list<co
     }
     return true;
 }
-kdn_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? KDN_OK : KDN_ERR_CUDA; }
+kdn_status_t cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return KDN_OK;
+    (void)cudaGetLastError();              // reported by the status, not to whichever launch asks next
+    return KDN_ERR_CUDA;
+}
 
 kdn_status_t check_sizes(int H, int d_k, int d_v, kdn_dtype_t dtype, float scale, int decay) {
     if (H <= 0 || !isfinite(scale)) return KDN_ERR_INVALID_ARG;
@@ -167,7 +171,7 @@ kdn_status_t kdn_linear_backward(const kdn_linear_problem_t *p, const void *q, c
     if (!aligned({q, k, v, g, S0, d_o, dS_T, dq, dk, dv, dg, dS0})) return KDN_ERR_INVALID_ARG;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (a.nseq == 0 || a.ntok == 0) {
-        if (dg && a.decay == KDN_DECAY_HEAD && cudaMemsetAsync(dg, 0, sizeof(float) * a.H, cs) != cudaSuccess) return KDN_ERR_CUDA;
+        if (dg && a.decay == KDN_DECAY_HEAD && cuda_status(cudaMemsetAsync(dg, 0, sizeof(float) * a.H, cs)) != KDN_OK) return KDN_ERR_CUDA;
         if (a.nseq == 0 || !dS0) return KDN_OK;
     }
     if (a.ntok > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv || (a.decay != KDN_DECAY_NONE && !g)))
@@ -216,7 +220,7 @@ kdn_status_t kdn_layer_norm_backward(long long n, int G, int d, kdn_dtype_t dtyp
     if (!aligned({dy, x, weight, mean, rstd, dx, dweight, dbias})) return KDN_ERR_INVALID_ARG;
     if (n == 0) {   // no rows: the sums are zero
         for (float *out : {dweight, dbias})
-            if (out && cudaMemsetAsync(out, 0, sizeof(float) * (size_t)G * d, cs) != cudaSuccess) return KDN_ERR_CUDA;
+            if (out && cuda_status(cudaMemsetAsync(out, 0, sizeof(float) * (size_t)G * d, cs)) != KDN_OK) return KDN_ERR_CUDA;
         return KDN_OK;
     }
     if (!dy || !x || !mean || !rstd || !dx) return KDN_ERR_INVALID_ARG;

@@ -486,8 +486,7 @@ cudaError_t launch_linear_tc_backward(const LinBwdArgs &b, void *workspace, cuda
     KernelSetup ks;
     e = kernel_setup(reinterpret_cast<const void *>(kern), Smem::TOTAL, NT, false, &ks);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(lin_slots(a.cu != nullptr, a.T, a.ntok, a.nseq, C) * a.H), NT, Smem::TOTAL, st>>>(f);
-    e = cudaGetLastError();
+    e = launch(kern, dim3((unsigned)(lin_slots(a.cu != nullptr, a.T, a.ntok, a.nseq, C) * a.H)), NT, Smem::TOTAL, st, f);
     if (e != cudaSuccess || !b.dg || a.decay != KDN_DECAY_HEAD) return e;
     return launch_linear_head_decay(a, f.s.share, b.dg, C, st);
 }

@@ -140,11 +140,7 @@ namespace {
 template <int DK, int DVT, typename Tin>
 cudaError_t run(const LinArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)((long long)a.nseq * a.H * (a.dv / DVT));
-    if (!a.cu && a.T == 1)
-        linear_recurrent_kernel<DK, DVT, 1, Tin><<<grid, NT, 0, st>>>(a);
-    else
-        linear_recurrent_kernel<DK, DVT, 4, Tin><<<grid, NT, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch(!a.cu && a.T == 1 ? linear_recurrent_kernel<DK, DVT, 1, Tin> : linear_recurrent_kernel<DK, DVT, 4, Tin>, grid, NT, 0, st, a);
 }
 template <int DK, typename Tin>
 cudaError_t by_tile(const LinArgs &a, cudaStream_t st) {

@@ -278,8 +278,7 @@ cudaError_t run(const LinBwdArgs &b, float *share, cudaStream_t st) {
     auto kern = linear_short_backward_kernel<CS, DK, DVT, Tin>;
     const cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), smem, 16 * CS, false, &ks);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)b.a.nseq * b.a.H), 16 * CS, smem, st>>>(b, share);
-    return cudaGetLastError();
+    return launch(kern, dim3((unsigned)((long long)b.a.nseq * b.a.H)), 16 * CS, smem, st, b, share);
 }
 template <int DK, int DVT, typename Tin>
 cudaError_t by_length(const LinBwdArgs &b, float *share, cudaStream_t st) {

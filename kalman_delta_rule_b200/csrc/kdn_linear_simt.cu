@@ -552,8 +552,7 @@ __global__ void __launch_bounds__(256) linear_head_decay_kernel(LinArgs a, const
 
 // ------------------------------------------------------------------ host side
 cudaError_t launch_linear_head_decay(const LinArgs &a, const float *share, float *dg, int tokens, cudaStream_t st) {
-    linear_head_decay_kernel<<<a.H, 256, 0, st>>>(a, share, dg, (int)lin_slots(a.cu != nullptr, a.T, a.ntok, a.nseq, tokens), tokens);
-    return cudaGetLastError();
+    return launch(linear_head_decay_kernel, dim3((unsigned)a.H), 256, 0, st, a, share, dg, (int)lin_slots(a.cu != nullptr, a.T, a.ntok, a.nseq, tokens), tokens);
 }
 
 namespace {
@@ -571,8 +570,7 @@ cudaError_t deltas(const LinArgs &a, const Walks &ws, int walks, float2 *dec, cu
     auto kern = linear_delta_kernel<DK, DVT>;
     const cudaError_t e = kernel_setup(reinterpret_cast<const void *>(kern), smem, NT, false, &ks);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT, walks), NT, smem, st>>>(a, ws, dec);
-    return cudaGetLastError();
+    return launch(kern, dim3((unsigned)(slots_of(a) * a.H), a.dv / DVT, walks), NT, smem, st, a, ws, dec);
 }
 cudaError_t scans(const LinArgs &a, const Walks &ws, int walks, const float2 *dec, cudaStream_t st) {
     const long long threads = (long long)a.nseq * a.H * (a.dk * a.dv / 4);

@@ -705,8 +705,7 @@ size_t totals_bytes(const LinArgs &a, int sub) {
 size_t decay_bytes(const LinArgs &a) { return round256((size_t)slots(a, C) * a.H * sizeof(Decay)); }
 cudaError_t decays(const LinArgs &a, void *ws, cudaStream_t st) {
     const long long n = slots(a, C) * a.H;
-    linear_decay_kernel<<<(unsigned)((n + 7) / 8), 256, 0, st>>>(a, static_cast<Decay *>(ws), n);
-    return cudaGetLastError();
+    return launch(linear_decay_kernel, dim3((unsigned)((n + 7) / 8)), 256, 0, st, a, static_cast<Decay *>(ws), n);
 }
 
 template <typename K>
@@ -717,19 +716,12 @@ cudaError_t setup(K kern, size_t smem, int threads) {
 
 // `early`: right behind the decay launch; the CTAs may then start before it is done (they wait for it before they read
 // its records, and touch nothing else that it does)
-template <typename K, typename A>
-cudaError_t launch(K kern, long long grid, int threads, size_t smem, const A &args, bool early, cudaStream_t st) {
-    if (early) return launch_next(kern, dim3((unsigned)grid), threads, smem, st, args);
-    kern<<<(unsigned)grid, threads, smem, st>>>(args);
-    return cudaGetLastError();
-}
-
 template <bool REV, bool TOTALS>
 cudaError_t states(const StateArgs &f, bool early, cudaStream_t st) {
     auto kern = f.a.dk > 64 ? linear_state_kernel<REV, TOTALS, 2> : linear_state_kernel<REV, TOTALS, 1>;
     const cudaError_t e = setup(kern, StateSmem::TOTAL, NT_S);
     if (e != cudaSuccess) return e;
-    return launch(kern, slots(f.a, f.piece) * f.a.H * tiles_of(f.a), NT_S, StateSmem::TOTAL, f, early, st);
+    return launch_with(early, kern, dim3((unsigned)(slots(f.a, f.piece) * f.a.H * tiles_of(f.a))), NT_S, StateSmem::TOTAL, st, f);
 }
 
 // totals of the earlier segments into ws, if the sequences are cut
@@ -776,7 +768,7 @@ cudaError_t launch_linear_tc(const LinArgs &a, void *workspace, cudaStream_t st)
     auto kern = a.dk > 64 ? linear_forward_kernel<2> : linear_forward_kernel<1>;
     if (e == cudaSuccess) e = setup(kern, FwdSmem::TOTAL, NT_F);
     if (e != cudaSuccess) return e;
-    return launch(kern, slots(a, f.sp.seg) * a.H * tiles_of(a), NT_F, FwdSmem::TOTAL, f, !is_split(a, f.sp.seg), st);
+    return launch_with(!is_split(a, f.sp.seg), kern, dim3((unsigned)(slots(a, f.sp.seg) * a.H * tiles_of(a))), NT_F, FwdSmem::TOTAL, st, f);
 }
 
 namespace lin {

@@ -2,7 +2,8 @@
 // native step: contiguous tensors of the expected types and shapes on the current device, on its current stream.  Small
 // problems (a decode step's kernel takes 3 us) are bound by what a call costs on the host, and reading five tensors'
 // properties from Python costs more than the launch: 12.0 us a decode call in all, 5.0 with this (layer norm 15.7 and 6.5).
-// A function returns None for any other call, having done nothing: binding.py then checks, dispatches or raises.
+// A function returns None for any other call, having done nothing: binding.py then checks, dispatches or raises.  A call that
+// the library began and could not finish raises here: made again, a decode step would take its token twice.
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -26,6 +27,21 @@ struct {
     decltype(&kdn_layer_norm_backward_workspace_size) layer_norm_backward_workspace_size;
     decltype(&kdn_layer_norm_backward) layer_norm_backward;
 } kdn;
+
+PyObject *error = nullptr;     // binding.KdnError(code, where)
+
+// what a status other than KDN_OK comes to: None where the library has refused the arguments (before any launch), else the error
+PyObject *refused(kdn_status_t st, const char *where) {
+    if (st == KDN_ERR_INVALID_ARG || st == KDN_ERR_UNSUPPORTED || st == KDN_ERR_WORKSPACE) Py_RETURN_NONE;
+    PyObject *e = error ? PyObject_CallFunction(error, "is", (int)st, where) : nullptr;
+    if (e) {
+        PyErr_SetObject(error, e);
+        Py_DECREF(e);
+    } else if (!PyErr_Occurred()) {
+        PyErr_Format(PyExc_RuntimeError, "%s: status %d", where, (int)st);
+    }
+    return nullptr;
+}
 
 const at::Tensor *tensor(PyObject *o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 bool is(const at::Tensor &t, at::ScalarType type, c10::Device dev) {
@@ -141,9 +157,9 @@ PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         sp = s.data_ptr();
     }
     const at::Tensor ws = need ? scratch(need, l.dev) : at::Tensor();
-    if (kdn.linear_forward(&l.p, l.q->data_ptr(), l.k->data_ptr(), l.v->data_ptr(), static_cast<float *>(l.g), static_cast<float *>(s0),
-                           o.data_ptr(), static_cast<float *>(sp), need ? ws.data_ptr() : nullptr, need, stream_of(l.dev)) != KDN_OK)
-        Py_RETURN_NONE;
+    const kdn_status_t st = kdn.linear_forward(&l.p, l.q->data_ptr(), l.k->data_ptr(), l.v->data_ptr(), static_cast<float *>(l.g), static_cast<float *>(s0),
+                           o.data_ptr(), static_cast<float *>(sp), need ? ws.data_ptr() : nullptr, need, stream_of(l.dev));
+    if (st != KDN_OK) return refused(st, "kdn_linear_forward");
     PyObject *r = PyTuple_New(2);
     if (!r) return nullptr;
     PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(o));
@@ -160,10 +176,10 @@ PyObject *linear_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *S = tensor(a[4]);
     at::Tensor o;
     if (!S || !is(*S, at::kFloat, l.dev, l.states) || !l.output(a[6], *l.v, &o)) Py_RETURN_NONE;
-    if (kdn.linear_decode_tokens(l.p.B, l.p.T, l.p.H, l.p.d_k, l.p.d_v, l.p.in_dtype, l.p.scale, l.p.decay, l.q->data_ptr(),
+    const kdn_status_t st = kdn.linear_decode_tokens(l.p.B, l.p.T, l.p.H, l.p.d_k, l.p.d_v, l.p.in_dtype, l.p.scale, l.p.decay, l.q->data_ptr(),
                                  l.k->data_ptr(), l.v->data_ptr(), static_cast<float *>(l.g), static_cast<float *>(S->data_ptr()),
-                                 o.data_ptr(), stream_of(l.dev)) != KDN_OK)
-        Py_RETURN_NONE;
+                                 o.data_ptr(), stream_of(l.dev));
+    if (st != KDN_OK) return refused(st, "kdn_linear_decode_tokens");
     return THPVariable_Wrap(o);
     END_HANDLE_TH_ERRORS
 }
@@ -192,12 +208,12 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (l.g) dg = floats(tensor(a[3])->sizes(), l.dev);
     if (a[9] == Py_True) dS0 = floats(l.states, l.dev);
     const at::Tensor ws = scratch(need, l.dev);
-    if (kdn.linear_backward(&l.p, l.q->data_ptr(), l.k->data_ptr(), l.v->data_ptr(), static_cast<float *>(l.g), static_cast<float *>(s0),
+    const kdn_status_t st = kdn.linear_backward(&l.p, l.q->data_ptr(), l.k->data_ptr(), l.v->data_ptr(), static_cast<float *>(l.g), static_cast<float *>(s0),
                             d_o->data_ptr(), static_cast<float *>(ds), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                             dg.defined() ? static_cast<float *>(dg.data_ptr()) : nullptr,
                             dS0.defined() ? static_cast<float *>(dS0.data_ptr()) : nullptr, ws.data_ptr(), need,
-                            stream_of(l.dev)) != KDN_OK)
-        Py_RETURN_NONE;
+                            stream_of(l.dev));
+    if (st != KDN_OK) return refused(st, "kdn_linear_backward");
     PyObject *r = PyDict_New();
     if (r && put(r, "dq", dq) && put(r, "dk", dk) && put(r, "dv", dv) && (!dg.defined() || put(r, "dg", dg)) &&
         (!dS0.defined() || put(r, "dS0", dS0)))
@@ -253,10 +269,10 @@ PyObject *layer_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const at::IntArrayRef rows = r.x->sizes().slice(0, r.x->dim() - 1);
     at::Tensor mean = floats(rows, r.dev), rstd = floats(rows, r.dev);
-    if (kdn.layer_norm(r.n, r.G, r.d, (kdn_dtype_t)r.code, eps, r.x->data_ptr(), w ? static_cast<float *>(w->data_ptr()) : nullptr,
+    const kdn_status_t st = kdn.layer_norm(r.n, r.G, r.d, (kdn_dtype_t)r.code, eps, r.x->data_ptr(), w ? static_cast<float *>(w->data_ptr()) : nullptr,
                        b ? static_cast<float *>(b->data_ptr()) : nullptr, y.data_ptr(), static_cast<float *>(mean.data_ptr()),
-                       static_cast<float *>(rstd.data_ptr()), stream_of(r.dev)) != KDN_OK)
-        Py_RETURN_NONE;
+                       static_cast<float *>(rstd.data_ptr()), stream_of(r.dev));
+    if (st != KDN_OK) return refused(st, "kdn_layer_norm");
     PyObject *t = PyTuple_New(3);
     if (!t) return nullptr;
     PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(y));
@@ -284,12 +300,12 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         db = floats(w->sizes(), r.dev);
         ws = scratch(need, r.dev);
     }
-    if (kdn.layer_norm_backward(r.n, r.G, r.d, (kdn_dtype_t)r.code, dy->data_ptr(), r.x->data_ptr(),
+    const kdn_status_t st = kdn.layer_norm_backward(r.n, r.G, r.d, (kdn_dtype_t)r.code, dy->data_ptr(), r.x->data_ptr(),
                                 w ? static_cast<float *>(w->data_ptr()) : nullptr, static_cast<float *>(mean->data_ptr()),
                                 static_cast<float *>(rstd->data_ptr()), dx.data_ptr(), w ? static_cast<float *>(dw.data_ptr()) : nullptr,
                                 w ? static_cast<float *>(db.data_ptr()) : nullptr, w ? ws.data_ptr() : nullptr, need,
-                                stream_of(r.dev)) != KDN_OK)
-        Py_RETURN_NONE;
+                                stream_of(r.dev));
+    if (st != KDN_OK) return refused(st, "kdn_layer_norm_backward");
     PyObject *d = PyDict_New();
     if (d && put(d, "dx", dx) && (!w || (put(d, "dweight", dw) && put(d, "dbias", db)))) return d;
     Py_XDECREF(d);
@@ -312,8 +328,18 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// raise_with(type): the error that a failed call raises, made from (status, name of the function)
+PyObject *raise_with(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 1 || !PyExceptionClass_Check(a[0])) {
+        PyErr_SetString(PyExc_TypeError, "raise_with() takes an exception type");
+        return nullptr;
+    }
+    Py_XSETREF(error, Py_NewRef(a[0]));
+    Py_RETURN_NONE;
+}
+
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(bind), METHOD(linear_forward), METHOD(linear_decode), METHOD(linear_backward),
+PyMethodDef methods[] = {METHOD(bind), METHOD(raise_with), METHOD(linear_forward), METHOD(linear_decode), METHOD(linear_backward),
                          METHOD(layer_norm), METHOD(layer_norm_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kdn_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

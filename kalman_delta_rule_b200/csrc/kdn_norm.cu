@@ -423,19 +423,9 @@ cudaError_t run(const NormArgs &a, bool back, cudaStream_t st) {
     const size_t smem = back ? Ahead<T, VEC, LPR, EPL, 2, 2>::BYTES : Ahead<T, VEC, LPR, EPL, 1, 0>::BYTES;
     cudaError_t e = blocks_for(kern, smem, Sh::NT, a, Sh::ROWS, &blocks);
     if (e != cudaSuccess) return e;
-    kern<<<blocks, Sh::NT, smem, st>>>(a);
-    e = cudaGetLastError();
+    e = launch(kern, dim3((unsigned)blocks), Sh::NT, smem, st, a);
     if (e != cudaSuccess || !back || !a.part) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.d + 31) / 32, a.G, 2);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_params_kernel, a, blocks);
+    return launch_next(norm_params_kernel, dim3((a.d + 31) / 32, a.G, 2), 1024, 0, st, a, blocks);
 }
 
 // Within a warp 16 elements per thread (8 for the narrowest rows): against 8, a row of 128 costs a quarter fewer
@@ -457,7 +447,7 @@ cudaError_t by_width(const NormArgs &a, bool back, cudaStream_t st) {
     return run<T, VEC, 1024, 16>(a, back, st);
 }
 // (bf16 rows of an even width in pairs: 50000 x 510 21.4 us, element by element 38.6)
-cudaError_t launch(const NormArgs &a, bool bf16_in, bool back, cudaStream_t st) {
+cudaError_t by_type(const NormArgs &a, bool bf16_in, bool back, cudaStream_t st) {
     if (bf16_in) {
         if (a.d % 8 == 0) return by_width<bf16, 8>(a, back, st);
         return a.d % 2 == 0 ? by_width<bf16, 2>(a, back, st) : by_width<bf16, 1>(a, back, st);
@@ -470,7 +460,7 @@ cudaError_t launch(const NormArgs &a, bool bf16_in, bool back, cudaStream_t st) 
 size_t norm_backward_workspace_bytes(long long n, int G, int d) {
     return (size_t)(G > kMaxBlocks ? G : kMaxBlocks / G * G) * 2 * d * sizeof(float);
 }
-cudaError_t launch_norm(const NormArgs &a, bool bf16_in, cudaStream_t st) { return launch(a, bf16_in, false, st); }
-cudaError_t launch_norm_backward(const NormArgs &a, bool bf16_in, cudaStream_t st) { return launch(a, bf16_in, true, st); }
+cudaError_t launch_norm(const NormArgs &a, bool bf16_in, cudaStream_t st) { return by_type(a, bf16_in, false, st); }
+cudaError_t launch_norm_backward(const NormArgs &a, bool bf16_in, cudaStream_t st) { return by_type(a, bf16_in, true, st); }
 
 }  // namespace kdn
