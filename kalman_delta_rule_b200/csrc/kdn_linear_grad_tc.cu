@@ -3,8 +3,9 @@
 // sequence (kdn_linear_tc.cu); everything else is parallel over (chunk, head), one CTA each.  With
 // a_t = scale e^{G_t}, w_t = e^{G_C - G_t}, P = scale Q K^T o D, dP = dO V^T, dA = scale dP o D, Z = P o dP:
 //     dQ = dA K + a (dO S^T),   dK = dA^T Q + w (V R^T),   dV = P^T dO + w (K R)
-//     dg_t = sum_{s >= t} (rows Z - columns Z)_s + sum_{s >= t} q_s.(a dO S^T)_s + sum_{s < t} k_s.(w V R^T)_s + e^{G_C} <S, R>
-// (no term is divided by a decay; none of the four sums cancels against another).
+//     dg_t = sum_{i >= t, j < t} Z_ij + sum_{s >= t} q_s.(a dO S^T)_s + sum_{s < t} k_s.(w V R^T)_s + e^{G_C} <S, R>
+// (no term is divided by a decay, and every sum is formed from its own terms: as a difference of larger sums -- rows of Z less
+// columns of Z, say -- a reset's gradient would be their roundings instead of zero).
 //
 // TMEM holds four accumulators of 128 columns: the scores, dP, dO S^T and V R^T.  The last two are scaled
 // by their rows' decays in place, and dA K and dA^T Q are added to them; the first two are replaced by the
@@ -222,10 +223,12 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             }
         }
     }
-    // ---- P and dA (bf16) to shared memory; the rows' and columns' sums of Z
+    // ---- P and dA (bf16) to shared memory; of Z, per block of 32 rows (q4) x 32 columns (cg): the rows' sums (zr), and for each
+    // column t the sum over the rows from t on of the block's columns before t (zc); the sums of whole blocks behind the diagonal's
+    // neighbours
     const float since = decay_since(d, row), until = decay_until(d, row);
     {
-        f32x2 z2 = pk2(0.f, 0.f);
+        float z = 0.f;                        // of the row's columns so far
         const float fs = a.scale * since;
         const f32x2 fs2 = pk2(fs, fs);
 #pragma unroll 1
@@ -260,12 +263,17 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
                     for (int i = 0; i < 2; ++i) {
                         const int k = j + 2 * i;
                         const f32x2 v = pk2(y[k], y[k + 1]), pp = mul2(pk2(x[k], x[k + 1]), g[i]), zz = mul2(pp, v);
+                        const float before = z + x2(zz);
                         pb[k / 2] = round_bf16x2(pp);
                         ab[k / 2] = round_bf16x2(mul2(v, g[i]));
-                        z2 = add2(z2, zz);
-                        x[k] = x2(zz);
-                        x[k + 1] = y2(zz);
+                        x[k] = z;
+                        x[k + 1] = before;
+                        z = before + y2(zz);
                     }
+                }
+                if (cg == q4) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = p + j <= lane ? x[j] : 0.f;
                 }
                 const float s = sum16(x, lane);
                 if (!(lane & 1)) zc[q4 * C + c0 + (lane >> 1)] = s;
@@ -280,7 +288,11 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
                 *reinterpret_cast<uint4 *>(sm + L_::DA + tile + off) = make_uint4(ab[4 * j], ab[4 * j + 1], ab[4 * j + 2], ab[4 * j + 3]);
             }
         }
-        zr[cg * C + row] = x2(z2) + y2(z2);
+        zr[cg * C + row] = z;
+        if (q4 > cg + 1) {                    // (cg, q4) = (0, 2), (0, 3), (1, 3)
+            z = warp_sum(z);
+            if (lane == 0) sr_w[26 + cg + q4] = z;
+        }
     }
     wait_tma();
     zero_tail(L_::Q, KATOMS);
@@ -342,12 +354,17 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
         mma_tiles<8, true, true, NK>(T_DK, sb + L_::DA, sb + L_::Q, true);
         mma_commit(bar_c);                    // (a barrier of its own: it must not run a phase ahead of a waiter)
     }
-    // meanwhile four warps sum up the decay's gradient, a token per thread: sums over the tokens from t on and before t
+    // meanwhile four warps sum up the decay's gradient, a token per thread: sums over the tokens from t on and before t.  Pairs
+    // (i, j): within the warp's columns (zc), its rows from t on with the columns before them, later rows with those
     if (f.b.dg && warp < 4) {
         const int t = threadIdx.x;
-        float later = 0.f, earlier = 0.f, s0 = 0.f;
+        float pairs = 0.f, rows = 0.f, later = 0.f, earlier = 0.f, s0 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) later += zr[i * C + t] - zc[i * C + t];
+        for (int i = 0; i < 4; ++i) {
+            pairs += zc[i * C + t];
+            if (i < warp) rows += zr[i * C + t];
+        }
+        if (warp == 1 || warp == 2) pairs += sr_w[27 + warp] + sr_w[28 + warp];
 #pragma unroll
         for (int i = 0; i < 2 * KATOMS; ++i) {
             later += xi[i * C + t];
@@ -358,23 +375,27 @@ __global__ void __launch_bounds__(NT, 1) linear_grad_tc_kernel(const __grid_cons
             const float4 x = *reinterpret_cast<const float4 *>(sr_w + i);
             s0 += (x.x + x.y) + (x.z + x.w);
         }
-        const float own = earlier;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const float yl = __shfl_down_sync(0xffffffffu, later, off), ye = __shfl_up_sync(0xffffffffu, earlier, off);
-            if (lane + off < 32) later += yl;
+            const float yr = __shfl_down_sync(0xffffffffu, rows, off), yl = __shfl_down_sync(0xffffffffu, later, off),
+                        ye = __shfl_up_sync(0xffffffffu, earlier, off);
+            if (lane + off < 32) {
+                rows += yr;
+                later += yl;
+            }
             if (lane >= off) earlier += ye;
         }
         if (lane == 0) sr_w[16 + warp] = later;          // the warp's sums
         if (lane == 31) sr_w[20 + warp] = earlier;
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        earlier -= own;
+        earlier = __shfl_up_sync(0xffffffffu, earlier, 1);   // of the tokens before
+        if (lane == 0) earlier = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i > warp) later += sr_w[16 + i];
             if (i < warp) earlier += sr_w[20 + i];
         }
-        const float g = (later + earlier) + d.whole.x * s0;
+        const float g = ((pairs + rows) + later) + earlier + d.whole.x * s0;
         if (a.decay == KDN_DECAY_TOKEN) {
             if (t < L) f.b.dg[(size_t)(tok + t) * a.H + h] = g;
         } else {

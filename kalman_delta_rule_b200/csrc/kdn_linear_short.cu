@@ -248,19 +248,20 @@ __global__ void __launch_bounds__(16 * CS, 32 / CS) linear_short_backward_kernel
             before += ys[lane / TG * WG + w][lane % TG];
         }
     }
-    const float own = before;
 #pragma unroll
     for (int off = 1; off < CS; off <<= 1) {
         const float x = __shfl_down_sync(0xffffffffu, later, off), y = __shfl_up_sync(0xffffffffu, before, off);
         if (lane + off < 32) later += x;
         if (lane >= off) before += y;
     }
+    before = __shfl_up_sync(0xffffffffu, before, 1);     // of the tokens before
+    if (lane == 0) before = 0.f;
     __syncwarp();
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) s0 += srs[w];
     if (lane < len) {
         for (int i = lane; i < len; ++i) g += Z[i][lane];
-        g = fmaf(whole, s0, (g + later) + (before - own));
+        g = fmaf(whole, s0, (g + later) + before);
         if (a.decay == KDN_DECAY_TOKEN) b.dg[(size_t)(t0 + lane) * a.H + h] = g;
     }
     if (a.decay == KDN_DECAY_HEAD) {

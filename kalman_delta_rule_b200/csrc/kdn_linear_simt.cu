@@ -334,8 +334,9 @@ __global__ void __launch_bounds__(NT) linear_out_kernel(LinArgs a, const float *
 // R the gradient of the state at its end, a_t = scale e^{G_t}, w_t = e^{G_C - G_t}:
 //   dQ = dA K + a (dO S^T),  dK = dA^T Q + w (V R^T),  dV = P^T dO + w (K R)
 //   dg_t = sum over pairs (query i >= t, key j < t), in the chunk, before and behind it:
-//        sum_{s >= t} (rows Z - columns Z)_s + sum_{s >= t} q_s.(a dO S^T)_s + sum_{s < t} k_s.(w V R^T)_s + e^{G_C} <S, R>
-// No term is divided by a decay, and none of the four cancels against another.
+//        sum_{i >= t, j < t} Z_ij + sum_{s >= t} q_s.(a dO S^T)_s + sum_{s < t} k_s.(w V R^T)_s + e^{G_C} <S, R>
+// No term is divided by a decay, and every sum is formed from its own terms (a difference of larger ones would leave their
+// roundings where a reset's gradient is zero).
 template <int DK, int DVT, bool FOLD>
 __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBwdArgs b, Ws ws)
 {
@@ -344,10 +345,12 @@ __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBw
     extern __shared__ __align__(16) float sm[];
     float *Qs = sm, *Ks = Qs + C * (DK + PAD), *Vs = Ks + C * (DK + PAD), *Os = Vs + C * (DVT + PAD),
           *Ss = Os + C * (DVT + PAD), *Ps = Ss + DK * (DVT + PAD);
-    float *const Rs = Ss, *const As = Ps;   // each takes the other's place once that has been read
+    float *const Rs = Ss, *const As = Ps, *const Zs = Vs;   // each takes the other's place once that has been read
+    constexpr int ZR = C + 1;              // Z's row stride
+    static_assert(C * ZR <= 2 * C * (DVT + PAD) + DK * (DVT + PAD), "Z takes the place of V, dO and the states");
     __shared__ ChunkDecay dec_s;
     const Log2 *G = dec_s.G;
-    __shared__ float zr[C], zc[8][C], xi[C], yi[C], wsum[8];
+    __shared__ float zc[4][C], xi[C], yi[C], wsum[8];
     const int u = blockIdx.x / a.H, h = blockIdx.x % a.H;
     LinPiece p;
     if (!lin_piece(a, u, C, p)) return wait_for_launch();
@@ -445,22 +448,17 @@ __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBw
         }
     }
 
-    // ---- dA to shared memory; rows and columns of Z; the boundary terms of the decay's gradient
-    __syncthreads();           // P has been read
-    float zcol[4] = {};
+    // ---- dA and Z to shared memory; the boundary terms of the decay's gradient
+    __syncthreads();           // P and the last tile have been read
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = ty * 4 + i;
-        float z = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int s = tx + 16 * j;
             As[t * (C + PAD) + s] = s <= t ? scale * dp[i][j] * lin_exp2_between(G[t], G[s]) : 0.f;
-            const float zz = s <= t ? pv[i][j] * dp[i][j] : 0.f;
-            z += zz;
-            zcol[j] += zz;
+            Zs[t * ZR + s] = s <= t ? pv[i][j] * dp[i][j] : 0.f;
         }
-        z = row_sum(z);
         const float fa = scale * lin_exp2(G[t]), fw = lin_exp2_between(G[C - 1], G[t]);
         float x = 0.f, y = 0.f;
 #pragma unroll
@@ -472,16 +470,32 @@ __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBw
         }
         x = row_sum(x);
         y = row_sum(y);
-        if (tx == 0) { zr[t] = z; xi[t] = x; yi[t] = y; }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float z = zcol[j] + __shfl_xor_sync(0xffffffffu, zcol[j], 16);
-        if (lane < 16) zc[warp][tx + 16 * j] = z;
+        if (tx == 0) { xi[t] = x; yi[t] = y; }
     }
     sr = warp_sum(sr);
     if (lane == 0) wsum[warp] = sr;
     __syncthreads();
+    if (b.dg) {                // sum_{i >= t, j < t} Z_ij: Z's rows become the sums of the columns before, then columns from the diagonal down
+        float *z = Zs + (threadIdx.x >> 2) * ZR + (threadIdx.x & 3) * 16, run = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) run += z[j];
+        const float a1 = __shfl_up_sync(0xffffffffu, run, 1, 4), a2 = __shfl_up_sync(0xffffffffu, run, 2, 4), a3 = __shfl_up_sync(0xffffffffu, run, 3, 4);
+        const int part = threadIdx.x & 3;
+        run = part == 0 ? 0.f : part == 1 ? a1 : part == 2 ? a2 + a1 : (a3 + a2) + a1;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float own = z[j];
+            z[j] = run;
+            run += own;
+        }
+        __syncthreads();
+        const int t = threadIdx.x % C, i0 = (threadIdx.x / C) * 16;
+        run = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) run += i0 + i >= t ? Zs[(i0 + i) * ZR + t] : 0.f;
+        zc[threadIdx.x / C][t] = run;
+        __syncthreads();
+    }
 
     mm<NK, false, false>(dqi, As, C + PAD, Ks, DK + PAD, C, ty, tx);
     mm<NK, true, false>(dki, As, C + PAD, Qs, DK + PAD, C, ty, tx);
@@ -500,26 +514,26 @@ __global__ void __launch_bounds__(NT, DK <= 64 ? 2 : 1) linear_grad_kernel(LinBw
         float s0 = 0.f;
         for (int w = 0; w < 8; ++w) s0 += wsum[w];
         const double whole = (double)lin_exp2(G[C - 1]) * s0;
-        double later[2], earlier[2];
+        double pairs[2], later[2], earlier[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int t = 2 * lane + e;
-            float z = 0.f;
-            for (int w = 0; w < 8; ++w) z += zc[w][t];
-            later[e] = (double)zr[t] - z + xi[t];
+            pairs[e] = (zc[0][t] + zc[1][t]) + (zc[2][t] + zc[3][t]);
+            later[e] = xi[t];
             earlier[e] = yi[t];
         }
-        double sl = later[0] + later[1], se = earlier[0] + earlier[1];
-        double fl = sl, fe = se;
+        double fl = later[0] + later[1], fe = earlier[0] + earlier[1];
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const double yl = __shfl_down_sync(0xffffffffu, fl, off), ye = __shfl_up_sync(0xffffffffu, fe, off);
             if (lane + off < 32) fl += yl;
             if (lane >= off) fe += ye;
         }
-        fl -= sl;              // tokens of the lanes above
-        fe -= se;              // tokens of the lanes below
-        const double d1 = whole + fl + later[1] + fe + earlier[0], d0 = whole + fl + later[1] + later[0] + fe;
+        fl = __shfl_down_sync(0xffffffffu, fl, 1);   // tokens of the lanes above
+        fe = __shfl_up_sync(0xffffffffu, fe, 1);     // tokens of the lanes below
+        if (lane == 31) fl = 0.0;
+        if (lane == 0) fe = 0.0;
+        const double d1 = whole + pairs[1] + fl + later[1] + fe + earlier[0], d0 = whole + pairs[0] + fl + later[1] + later[0] + fe;
         if (a.decay == KDN_DECAY_TOKEN) {
             if (2 * lane < L) b.dg[(size_t)(tok + 2 * lane) * a.H + h] = (float)d0;
             if (2 * lane + 1 < L) b.dg[(size_t)(tok + 2 * lane + 1) * a.H + h] = (float)d1;
