@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
             if (!w.wait(dec_full + st, (c >> 1) & 1) || !w.wait(v_full + st, (c >> 1) & 1)) break;
             const Decay &d = dec[st];
             const bool factored = d.factored;
-            const float until = decay_until(d, row);
+            const float until = decay_until(d, row), since = factored ? 1.f / d.b[row] : 1.f;
             if (c >= 1 && !w.wait(dl_full, (c - 1) & 1)) break;   // the MMAs that read the weighted rows before
             if (row < L) {
                 weigh_row(sm + L_::V + st * ATOM, sm + L_::VP, row, half, until);
@@ -279,11 +279,17 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
                 if (c16 <= q4 * 32 + 31) {
                     float x[16];
                     tmem_ld16(T_SC + lanes + c16, x);
-                    if (factored) {
+                    if (factored) {                   // (the factors first: their product is at most one, 2^{-G_s} alone up to 2^60)
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 b = *reinterpret_cast<const float4 *>(d.b + c16 + j);
-                            x[j] *= b.x; x[j + 1] *= b.y; x[j + 2] *= b.z; x[j + 3] *= b.w;
+                            if constexpr (KATOMS == 1) {      // (in pairs it costs this instance 16 bytes of spills: 65.8 -> 67.5 us)
+                                x[j] *= since * b.x; x[j + 1] *= since * b.y; x[j + 2] *= since * b.z; x[j + 3] *= since * b.w;
+                            } else {
+                                const f32x2 y = mul2(pk2(x[j], x[j + 1]), mul2(pk2(since, since), pk2(b.x, b.y))),
+                                            z = mul2(pk2(x[j + 2], x[j + 3]), mul2(pk2(since, since), pk2(b.z, b.w)));
+                                x[j] = x2(y); x[j + 1] = y2(y); x[j + 2] = x2(z); x[j + 3] = y2(z);
+                            }
                         }
                     } else {
 #pragma unroll
@@ -352,10 +358,9 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
         for (int c = 0; c < n; ++c) {
             const int st = c & 1, L = min(C, len - c * C);
             if (!w.wait(dec_full + st, (c >> 1) & 1)) break;
-            // factored: the row's 2^{G_t} is common to both parts of o (P holds the columns' 2^{-G_s})
-            const float fs = a.scale * decay_since(dec[st], row), fi = dec[st].factored ? fs : a.scale;
+            const float fs = a.scale * decay_since(dec[st], row);
             warp_arrive(dec_free + st);
-            const f32x2 fs2 = pk2(fs, fs), fi2 = pk2(fi, fi);
+            const f32x2 fs2 = pk2(fs, fs), fi2 = pk2(a.scale, a.scale);
             if (!w.wait(o_full, c & 1)) break;
             tc_fence_after();
 #pragma unroll 2
