@@ -593,11 +593,18 @@ cudaError_t scans(const LinArgs &a, const Walks &ws, int walks, const float2 *de
 
 // Sequences of a few chunks go without the scan: its launch costs more than reading their contributions again does (256
 // tokens of 2 heads of 32: 14.4 -> 10.4 us; 512 of 1024 heads of 128, where most is read again: 4032 -> 3592; the gradient
-// of 5003 tokens in 24 sequences, H4 d64: 102 -> 97).  Packed lengths are known on the device only: a few chunks on
-// average, and not so many tokens in all that a single sequence of them would matter.
+// of 5003 tokens in 24 sequences, H4 d64: 96 -> 86).  Packed lengths are known on the device only: a few chunks on
+// average, and so little to read that one sequence of nearly all tokens, whose chunk j reads j contributions again, still costs
+// no more than about a quarter (4990 tokens beside 11 single ones, H4 d64: 61 -> 64 us, gradient 105 -> 132).  Both bounds are on
+// that sequence: what its last CTA reads in turn (past 1.5 MB: 4080 tokens of one head of 128 x 256, 8 MB: 67 -> 120 us) and what
+// all of them read (past 256 MB: 8170 tokens of 16 heads of 128 x 256, 17 GB: 2.3 -> 4.3 ms, gradient 2.9 -> 6.7).
 bool folded(const LinArgs &a) {
     constexpr int FEW = 8 * C;
-    return a.cu ? a.ntok <= FEW || (a.ntok <= 16 * FEW && a.ntok / FEW < a.nseq) : a.T <= FEW;
+    if (!a.cu) return a.T <= FEW;
+    if (a.ntok <= FEW) return true;
+    if (a.ntok > 16 * FEW || a.ntok / FEW >= a.nseq) return false;
+    const long long chunks = a.ntok / C, one = chunks * a.dk * a.dv * 4;
+    return one <= 3ll << 19 && one * chunks / 2 * a.H <= 256ll << 20;
 }
 
 template <int DK, int DVT, bool FOLD>
