@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(1024) norm_params_kernel(NormArgs a, int block
     if (c < a.d) {
         const float *p = a.part + (size_t)blockIdx.z * a.d + c;
 #pragma unroll 8
-        for (int b = g + part * a.G; b < blocks; b += 32 * a.G) s += __ldg(p + (size_t)b * 2 * a.d);
+        for (int b = g + part * a.G; b < blocks; b += 32 * a.G) s += __ldcg(p + (size_t)b * 2 * a.d);   // (not __ldg: written while this kernel waited)
     }
     red[part][lane] = s;
     __syncthreads();
