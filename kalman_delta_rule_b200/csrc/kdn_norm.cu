@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(Shape<LPR>::NT, Shape<LPR>::BWD) norm_backward
         w[e] = pk2(param(2 * e), param(2 * e + 1));
         dw[e] = db[e] = 0;
     }
-    // a place without an element or a row holds zeros: dy's make every term of it vanish
+    // a place without an element or a row holds zeros: dy's make every term of it vanish, but for 0 times an xh that has left
+    // fp32's range (a large mean in a row that hardly varies), which is looked for behind the sum
     extern __shared__ __align__(16) uint8_t mem[];
     typedef Ahead<T, VEC, LPR, EPL, 2, 2> Next;
     Next next{mem};
@@ -329,6 +330,14 @@ __global__ void __launch_bounds__(Shape<LPR>::NT, Shape<LPR>::BWD) norm_backward
         }
         s[0] = x2(s1) + y2(s1);
         s[1] = x2(s2) + y2(s2);
+        if (__builtin_expect(s[1] != s[1], 0)) {
+            s[1] = 0.f;
+#pragma unroll
+            for (int e = 0; e < EPL / 2; ++e) {
+                if ((2 * e / VEC * LPR + lane) * VEC < a.d) s[1] = fmaf(x2(u[e]), x2(xh[e]), s[1]);
+                if (((2 * e + 1) / VEC * LPR + lane) * VEC < a.d) s[1] = fmaf(y2(u[e]), y2(xh[e]), s[1]);
+            }
+        }
         sum(s);
         if (i >= a.n) continue;
         const f32x2 m1 = pk2(s[0] * inv, s[0] * inv), m2 = pk2(-s[1] * inv, -s[1] * inv);
