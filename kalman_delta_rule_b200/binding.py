@@ -7,7 +7,7 @@ The raw functions keep the C names (``kdn_forward_chunkwise``, ``kdn_decode_step
 calls: they allocate outputs and workspace with torch and pass the current stream.  So do
 ``linear_forward``, ``linear_backward``, ``linear_decode_step`` and ``linear_decode_tokens`` (linear
 attention with a decay for each head) and ``layer_norm`` and ``layer_norm_backward``, whose common call
-goes through the extension module ``_kdn_marshal.so`` instead of ctypes.
+goes through the extension module ``_kdn_marshal.so`` instead of ctypes (where it is built: it saves microseconds).
 Every step of the computation runs in the library's kernels; there is no CPU or
 PyTorch fallback -- a missing library or device raises.
 """
@@ -20,6 +20,7 @@ from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libkdn.so")
+MARSHAL_PATH = os.path.join(PKG, "_kdn_marshal.so")
 
 KDN_OK, KDN_ERR_INVALID_ARG, KDN_ERR_UNSUPPORTED, KDN_ERR_CUDA, KDN_ERR_TIMEOUT, KDN_ERR_RANGE, KDN_ERR_WORKSPACE = range(7)
 KDN_DTYPE_F32, KDN_DTYPE_BF16 = 0, 1
@@ -398,19 +399,41 @@ def _cuda():
     return _mod
 
 
+class _NoNative:
+    """In the place of an extension module that is not there: every call is left to the code here."""
+    linear_forward = linear_decode = linear_backward = layer_norm = layer_norm_backward = staticmethod(lambda *a: None)
+
+
+def _native_module(torch):
+    """The built extension module, or None (with a warning) if it is missing or was built for another torch."""
+    import importlib.util
+    import sys
+    import warnings
+    abi, why = f"{torch.__version__} {sys.implementation.cache_tag}", "is not built"
+    if os.path.exists(MARSHAL_PATH):
+        try:
+            spec = importlib.util.spec_from_file_location("_kdn_marshal", MARSHAL_PATH)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            if mod.abi == abi:
+                return mod
+            why = f"was built for {mod.abi}, this is {abi}"
+        except ImportError as e:
+            why = f"cannot be loaded ({e})"
+    warnings.warn(f"{MARSHAL_PATH} {why}; calls go through ctypes, several microseconds slower each "
+                  "(`python -m kalman_delta_rule_b200.build` builds it)")
+    return None
+
+
 def _native():
     """The extension module, bound to the loaded library's functions."""
     global _native_mod
     if _native_mod is None:
         lib = load()
-        _cuda()
-        path = os.path.join(PKG, "_kdn_marshal.so")
-        if not os.path.exists(path):
-            raise FileNotFoundError(f"{path} not built; run `python -m kalman_delta_rule_b200.build`")
-        import importlib.util
-        spec = importlib.util.spec_from_file_location("_kdn_marshal", path)
-        mod = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(mod)
+        mod = _native_module(_cuda())
+        if mod is None:
+            _native_mod = _NoNative
+            return _native_mod
         names = ("linear_workspace_size", "linear_forward", "linear_decode_tokens", "linear_backward_workspace_size",
                  "linear_backward", "layer_norm", "layer_norm_backward_workspace_size", "layer_norm_backward")
         mod.bind(*(ctypes.cast(getattr(lib, "kdn_" + n), _vp).value for n in names))

@@ -345,4 +345,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kdn_marshal", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kdn_marshal() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__kdn_marshal() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "abi", KDN_MARSHAL_ABI) < 0) Py_CLEAR(m);   // the torch and interpreter it was built for
+    return m;
+}
