@@ -428,17 +428,18 @@ def _native_module(torch):
 def _native():
     """The extension module, bound to the loaded library's functions."""
     global _native_mod
-    if _native_mod is None:
-        lib = load()
-        mod = _native_module(_cuda())
-        if mod is None:
-            _native_mod = _NoNative
-            return _native_mod
-        names = ("linear_workspace_size", "linear_forward", "linear_decode_tokens", "linear_backward_workspace_size",
-                 "linear_backward", "layer_norm", "layer_norm_backward_workspace_size", "layer_norm_backward")
-        mod.bind(*(ctypes.cast(getattr(lib, "kdn_" + n), _vp).value for n in names))
-        mod.raise_with(KdnError)
-        _native_mod = mod
+    lib, torch = load(), _cuda()
+    with _lock:
+        if _native_mod is None:
+            mod = _native_module(torch)
+            if mod is None:
+                _native_mod = _NoNative
+                return _native_mod
+            names = ("linear_workspace_size", "linear_forward", "linear_decode_tokens", "linear_backward_workspace_size",
+                     "linear_backward", "layer_norm", "layer_norm_backward_workspace_size", "layer_norm_backward")
+            mod.bind(*(ctypes.cast(getattr(lib, "kdn_" + n), _vp).value for n in names))
+            mod.raise_with(KdnError)
+            _native_mod = mod
     return _native_mod
 
 
