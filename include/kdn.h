@@ -246,8 +246,8 @@ kdn_status_t kdn_backward(const kdn_problem_t *p,
  *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t        (readout after the write)
  *
  * Layouts, types, sizes, packed sequences, streams, errors and ownership are those of the head of
- * this file; the log decay is always fp32; no output may alias an input (the state of the recurrent
- * form apart) or another output.  Tokens behind the last packed sequence are neither read
+ * this file; the log decay is always fp32; no output or workspace may share a byte with an input (the
+ * state of the recurrent form apart) or another output: such a call is refused.  Tokens behind the last packed sequence are neither read
  * nor written.  A sequence never sees another one's rows, whatever they hold; within a sequence a
  * non-finite input may also reach the outputs of the tokens shortly before it (those of its chunk,
  * up to 127 tokens). */
@@ -312,7 +312,7 @@ kdn_status_t kdn_linear_backward(const kdn_linear_problem_t *p, const void *q, c
  *     m = mean(x),  r = (mean((x - m)^2) + eps)^(-1/2),  y = (x - m) r * weight + bias
  *  x, y         : device [n, G, d] (dtype);  weight, bias : device fp32 [G, d], or NULL (1, 0)
  *  mean, rstd   : device fp32 [n, G], m and r for the backward, or NULL (not written)
- * 1 <= d <= 16384, G <= 65535, eps >= 0; every pointer 16-byte aligned; no output may alias an input. */
+ * 1 <= d <= 16384, G <= 65535, eps >= 0; every pointer 16-byte aligned; no output shares a byte with an input. */
 kdn_status_t kdn_layer_norm(long long n, int G, int d, kdn_dtype_t dtype, float eps, const void *x,
                             const float *weight, const float *bias, void *y, float *mean, float *rstd, void *stream);
 

@@ -16,17 +16,35 @@ bool aligned(std::initializer_list<const void *> ptrs) {   // 16 bytes; NULL pas
         if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
     return true;
 }
-// no output is an input or another output (kernels read inputs while other CTAs write); NULL passes
-bool distinct(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+bool overlap(const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+// no output (or workspace) shares a byte with an input or another output (kernels read inputs while other CTAs write)
+bool distinct(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
     for (auto o = outs.begin(); o != outs.end(); ++o) {
-        if (!*o) continue;
-        for (const void *in : ins)
-            if (*o == in) return false;
+        for (const Span &in : ins)
+            if (overlap(*o, in)) return false;
         for (auto other = outs.begin(); other != o; ++other)
-            if (*o == *other) return false;
+            if (overlap(*o, *other)) return false;
     }
     return true;
 }
+// bytes of a problem's arrays
+struct Sizes {
+    size_t qk, vo, g, state;
+    Sizes(const kdn::LinArgs &a, kdn_dtype_t dtype) {
+        const size_t rows = (size_t)a.ntok * a.H, e = dtype == KDN_DTYPE_BF16 ? 2 : 4;
+        qk = rows * a.dk * e;
+        vo = rows * a.dv * e;
+        g = a.decay == KDN_DECAY_TOKEN ? rows * 4 : a.decay == KDN_DECAY_HEAD ? (size_t)a.H * 4 : 0;
+        state = (size_t)a.nseq * a.H * a.dk * a.dv * 4;
+    }
+};
 kdn_status_t cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return KDN_OK;
     (void)cudaGetLastError();              // reported by the status, not to whichever launch asks next
@@ -123,7 +141,9 @@ kdn_status_t kdn_linear_forward(const kdn_linear_problem_t *p, const void *q, co
     if (!aligned({q, k, v, g, S0, o, S_out})) return KDN_ERR_INVALID_ARG;
     const size_t need = forward_bytes(p, a);
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return KDN_ERR_WORKSPACE;
-    if (!distinct({a.ntok ? o : nullptr, S_out}, {q, k, v, g, S0})) return KDN_ERR_INVALID_ARG;
+    const Sizes n(a, p->in_dtype);
+    if (!distinct({{o, n.vo}, {S_out, n.state}, {workspace, need}}, {{q, n.qk}, {k, n.qk}, {v, n.vo}, {g, n.g}, {S0, n.state}}))
+        return KDN_ERR_INVALID_ARG;
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0; a.o = o; a.S_out = S_out;
     a.err = kdn::error_word();
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -143,11 +163,13 @@ kdn_status_t kdn_linear_decode_tokens(int N, int n_tokens, int H, int d_k, int d
     if (N == 0 || n_tokens == 0) return KDN_OK;
     if ((long long)N * n_tokens > (1ll << 30) || (long long)N * H * (d_v / 32) >= (1ll << 31)) return KDN_ERR_UNSUPPORTED;
     if (!q || !k || !v || !S || !o || (decay != KDN_DECAY_NONE && !g)) return KDN_ERR_INVALID_ARG;
-    if (!aligned({q, k, v, g, S, o}) || !distinct({o, S}, {q, k, v, g})) return KDN_ERR_INVALID_ARG;
+    if (!aligned({q, k, v, g, S, o})) return KDN_ERR_INVALID_ARG;
     kdn::LinArgs a{};
     a.q = q; a.k = k; a.v = v; a.g = g; a.decay = decay; a.scale = scale;
     a.S0 = S; a.S_out = S; a.o = o;
     a.T = n_tokens; a.nseq = N; a.H = H; a.dk = d_k; a.dv = d_v; a.ntok = N * n_tokens;
+    const Sizes n(a, in_dtype);
+    if (!distinct({{o, n.vo}, {S, n.state}}, {{q, n.qk}, {k, n.qk}, {v, n.vo}, {g, n.g}})) return KDN_ERR_INVALID_ARG;
     return cuda_status(kdn::launch_linear_recurrent(a, in_dtype == KDN_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -176,10 +198,12 @@ kdn_status_t kdn_linear_backward(const kdn_linear_problem_t *p, const void *q, c
     }
     if (a.ntok > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv || (a.decay != KDN_DECAY_NONE && !g)))
         return KDN_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < backward_bytes(p, a) ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u))
-        return KDN_ERR_WORKSPACE;
-    if (a.ntok > 0 ? !distinct({dq, dk, dv, dg, dS0}, {q, k, v, g, S0, d_o, dS_T}) : dS0 == dS_T) return KDN_ERR_INVALID_ARG;
+    const size_t need = backward_bytes(p, a);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return KDN_ERR_WORKSPACE;
+    const Sizes n(a, p->in_dtype);
+    if (!distinct({{dq, n.qk}, {dk, n.qk}, {dv, n.vo}, {dg, n.g}, {dS0, n.state}, {workspace, need}},
+                  {{q, n.qk}, {k, n.qk}, {v, n.vo}, {g, n.g}, {S0, n.state}, {d_o, n.vo}, {dS_T, n.state}}))
+        return KDN_ERR_INVALID_ARG;
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0;
     a.err = kdn::error_word();
     b.d_o = d_o; b.dS_T = dS_T; b.dq = dq; b.dk = dk; b.dv = dv; b.dg = dg; b.dS0 = dS0;
@@ -196,7 +220,8 @@ kdn_status_t kdn_layer_norm(long long n, int G, int d, kdn_dtype_t dtype, float 
     if (st != KDN_OK) return st;
     if (n == 0) return KDN_OK;
     if (!x || !y || !aligned({x, weight, bias, y, mean, rstd})) return KDN_ERR_INVALID_ARG;
-    if (!distinct({y, mean, rstd}, {x, weight, bias})) return KDN_ERR_INVALID_ARG;
+    const size_t par = (size_t)G * d * 4, rows = (size_t)n * G, all = rows * d * (dtype == KDN_DTYPE_BF16 ? 2 : 4);
+    if (!distinct({{y, all}, {mean, rows * 4}, {rstd, rows * 4}}, {{x, all}, {weight, par}, {bias, par}})) return KDN_ERR_INVALID_ARG;
     kdn::NormArgs a{};
     a.x = x; a.weight = weight; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd;
     a.n = n; a.G = G; a.d = d; a.eps = eps;
@@ -225,13 +250,16 @@ kdn_status_t kdn_layer_norm_backward(long long n, int G, int d, kdn_dtype_t dtyp
     }
     if (!dy || !x || !mean || !rstd || !dx) return KDN_ERR_INVALID_ARG;
     kdn::NormArgs a{};
+    size_t need = 0;
     if (dweight || dbias) {
-        if (!workspace || workspace_bytes < kdn::norm_backward_workspace_bytes(n, G, d) ||
-            (reinterpret_cast<uintptr_t>(workspace) & 255u))
-            return KDN_ERR_WORKSPACE;
+        need = kdn::norm_backward_workspace_bytes(n, G, d);
+        if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return KDN_ERR_WORKSPACE;
         a.part = static_cast<float *>(workspace);
     }
-    if (!distinct({dx, dweight, dbias}, {dy, x, weight, mean, rstd})) return KDN_ERR_INVALID_ARG;
+    const size_t par = (size_t)G * d * 4, rows = (size_t)n * G, all = rows * d * (dtype == KDN_DTYPE_BF16 ? 2 : 4);
+    if (!distinct({{dx, all}, {dweight, par}, {dbias, par}, {workspace, need}},
+                  {{dy, all}, {x, all}, {weight, par}, {mean, rows * 4}, {rstd, rows * 4}}))
+        return KDN_ERR_INVALID_ARG;
     a.x = x; a.dy = dy; a.weight = weight; a.dx = dx;
     a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
     a.dweight = dweight; a.dbias = dbias;
