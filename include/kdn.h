@@ -247,8 +247,8 @@ kdn_status_t kdn_backward(const kdn_problem_t *p,
  *
  * Layouts, types, sizes, packed sequences, streams, errors and ownership are those of the head of
  * this file; the log decay is always fp32; no output or workspace may share a byte with an input (the
- * state of the recurrent form apart) or another output: such a call is refused.  Tokens behind the last packed sequence are neither read
- * nor written.  A sequence never sees another one's rows, whatever they hold; within a sequence a
+ * state of the recurrent form apart) or another output: such a call is refused.  Tokens behind the last packed sequence have no part in any
+ * result, whatever they hold (tiles of rows that reach behind it may be read), and their rows of the outputs are not written.  A sequence never sees another one's rows, whatever they hold; within a sequence a
  * non-finite input may also reach the outputs of the tokens shortly before it (those of its chunk,
  * up to 127 tokens). */
 typedef enum {

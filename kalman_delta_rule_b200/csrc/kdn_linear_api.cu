@@ -83,11 +83,13 @@ kdn_status_t check_problem(const kdn_linear_problem_t *p, kdn::LinArgs *a) {
 // being known on the device only), have paths of their own: one launch instead of two to five, no states written and read
 // between launches, and fp32 arithmetic whatever the type -- with a few hundred scores nothing averages the tensor cores'
 // roundings of them.  At d = 128, with 1 / 64 / 2048 heads in all:
-// Forward, token after token: 16 tokens 5.2 / 7.0 / 99 us in bf16 against 9.2 / 9.5 / 229 on the tensor cores, 32 tokens
-// 8.6 / 11.6 / 177 against 9.1 / 9.5 / 228, 64 tokens 15.5 / 21 / 329 against 8.7 / 9.4 / 230.  fp32, 64 tokens: 15.2 / 21 / 310
-// against 32 / 38 / 1172 in chunks; one head of d = 64 meets them at 128 tokens (25 against 22).
-// Backward, the whole sequence as one chunk: 16 tokens 24 / 24 / 271 us against 27 / 28 / 544 on the tensor cores, 32 tokens
-// 39 / 40 / 584 against 27 / 28 / 541 (d = 64: 17 / 17 / 255 against 23 / 23 / 302; fp32 in chunks: 65 / 79 / 1563).
+// Forward, token after token: 16 tokens 5.7 / 7.6 / 100 us in bf16 against 9.2 / 9.7 / 231 on the tensor cores, 32 tokens
+// 9.0 / 12.2 / 178 against 9.2 / 9.6 / 230, 64 tokens 15.5 / 21 / 319 against 9.2 / 9.7 / 232.  fp32, 64 tokens: 14.7 / 20.8 / 294
+// against 21.3 / 22.3 / 851 in chunks, d = 64: 12.7 / 13.1 / 103 against 14.7 / 15.4 / 190.  At d = 32 alone the chunks are the
+// quicker ones from about 40 tokens on (64 tokens: 13.5 / 14.7 / 77 against 8.6 / 9.6 / 80).
+// Backward, the whole sequence as one chunk: 16 tokens 24 / 24 / 273 us against 28 / 28 / 548 on the tensor cores, 24 tokens
+// 31 / 32 / 469 against 28 / 28 / 550, 32 tokens 40 / 40 / 587 against 28 / 28 / 545 (d = 64: 17 / 17 / 257 against 23 / 23 / 303;
+// fp32 in chunks: 55 / 67 / 1135).  Above some 20 tokens at d = 128 the bf16 call pays for its accuracy, not for its time.
 constexpr int kShortForwardBf16 = 32, kShortForwardF32 = 64;
 enum Path { SHORT, CUDA_CORES, TENSOR_CORES };
 int longest(const kdn::LinArgs &a) { return a.cu ? a.ntok : a.T; }

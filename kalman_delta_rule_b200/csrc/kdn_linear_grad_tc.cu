@@ -14,7 +14,7 @@
 // Per chunk and head at d = 128: 12 products of 128 x 128 x 128 (6100 cycles of MMA), 256 KB in (half of it the two fp32
 // states) and 96 KB out, 15000 cycles at an SM's share of HBM.  Its operands fill shared memory, so one CTA per SM walks its
 // phases one after the other -- the states' terms, P and dA, the decay's sums, the outputs -- in about 29000: 220 us for B4 H16
-// T4096 (tensor pipe 22% active, DRAM 40%), behind 58 and 60 us for the two walks.
+// T4096 (tensor pipe 22% active, DRAM 39%), behind 58 to 61 and 60 to 63 us for the two walks; a call takes 344 to 360.
 #include "kdn_launch.h"
 #include "kdn_linear_tc.cuh"
 

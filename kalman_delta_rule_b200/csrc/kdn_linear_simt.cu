@@ -12,8 +12,10 @@
 // few, long sequences fills the GPU as well as one of many short ones.  The backward's two
 // directions share the first two launches; a launch starts while the one before runs out, with the
 // caller's rows read before its results are waited for.  256 tokens of 2 heads of 32: 10.4 us, two
-// launches' latency.  Gradient of 24 ragged sequences, 5003 tokens of 4 heads of 64: 97-101 us, bound by
-// the fp32 products of `grad` (1.4 waves of its 408 CTAs, two per SM by shared memory; 54% issue activity).
+// launches' latency.  Gradient of 24 ragged sequences, 5003 tokens of 4 heads of 64: 95-97 us, bound by
+// the fp32 products of `grad` (1.4 waves of its 408 CTAs, two per SM by shared memory; 54% issue activity).  At size the products
+// are bound by their reads of shared memory (a 4 x 4 tile per thread, single elements of B): 256 tokens of 1024 heads of 128
+// 1650 us, their gradient 2530, against some 350 for the multiply-adds of the forward.
 #include "kdn_common.cuh"
 #include "kdn_launch.h"
 

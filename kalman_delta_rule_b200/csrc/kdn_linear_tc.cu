@@ -14,8 +14,8 @@
 // Its floor is one pass over q, k, v and o at HBM's rate.  The MMAs take about 1950 cycles per chunk and tile (scores
 // 512, Q S 384, delta 800 -- its A operand, K, meets three terms of the weighted rows in one product of 192 columns --, P V
 // 256), shared memory's reads for them and the warps' passes about 2900, and a chunk 3450: a role's own latencies (TMEM
-// loads, conversions, the fence before its mbarrier) do not overlap with themselves.  B4 H16 T4096 d128: 79 us, 3.0 TB/s with
-// the decays' launch; tensor pipe 38% active, DRAM 39%.  One CTA per SM; that problem's 128 chains leave 20 SMs idle.
+// loads, conversions, the fence before its mbarrier) do not overlap with themselves.  B4 H16 T4096 d128: 79 us, tensor pipe
+// 37% active, DRAM 38%; with the decays' launch a call takes 88 to 92, 3.0 to 3.1 TB/s.  One CTA per SM; that problem's 128 chains leave 20 SMs idle.
 // Rounding: P and the copy of S that Q reads are bf16 (o itself is); the state never is -- its products
 // take three-term weighted rows and it stays in fp32 registers, so it keeps fp32's accuracy over any length.
 //
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(NT_F, 1) linear_forward_kernel(const __grid_co
 // TOTALS: from zero, only the piece's final value and decay are kept (what a segment hands on); pieces of a
 // sequence's last (REV: first) segment have nobody to hand on to and are left out.  STATES: from the given
 // state and the totals of the segments before, every chunk's value is stored.
-// The delta MMAs (896 cycles per chunk) hide the two epilogues: prep and state each have their own eight
+// The delta MMAs (800 cycles per chunk) hide the two epilogues: prep and state each have their own eight
 // warps and a second buffer of weighted rows and of TMEM columns.
 template <bool REV, bool TOTALS, int KATOMS>
 __global__ void __launch_bounds__(NT_S, 1) linear_state_kernel(const __grid_constant__ StateArgs f)

@@ -1,7 +1,7 @@
 // The common call of the linear-attention and layer-norm wrappers of binding.py, from torch tensors to the C ABI, in one
 // native step: contiguous tensors of the expected types and shapes on the current device, on its current stream.  Small
 // problems (a decode step's kernel takes 3 us) are bound by what a call costs on the host, and reading five tensors'
-// properties from Python costs more than the launch: 12.0 us a decode call in all, 5.0 with this (layer norm 15.7 and 6.5).
+// properties from Python costs more than the launch: 12.0 us a decode call in all, 4.9 with this (layer norm 15.7 and 7.0).
 // A function returns None for any other call, having done nothing: binding.py then checks, dispatches or raises.  A call that
 // the library began and could not finish raises here: made again, a decode step would take its token twice.
 #include <ATen/ops/empty.h>

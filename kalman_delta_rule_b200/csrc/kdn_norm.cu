@@ -441,7 +441,8 @@ cudaError_t run(const NormArgs &a, bool back, cudaStream_t st) {
 // instructions, which is what bounds short rows.  Across a CTA the rows in flight per SM count, so CTAs are small: 16
 // elements per thread against 8 bring rows of 2048 bf16 from 21.6 to 15.9 us (10000 of them; gradient of 15000 x 1602 from
 // 65 to 43).  Odd widths, an element per load, are bound by their instructions, and 8 per thread are quicker (20000 x 1001
-// bf16 24.7 us against 31.2).
+// bf16 24.7 us against 31.2).  Above 8192 the 1024 threads of a row have 64 registers each, and the gradient spills: 2048
+// rows of 16384 bf16 take 134 us (forward 39), 4096 of 8192 61.
 template <typename T, int VEC>
 cudaError_t by_width(const NormArgs &a, bool back, cudaStream_t st) {
     if (a.d <= 64) return run<T, VEC, 8, 8>(a, back, st);
